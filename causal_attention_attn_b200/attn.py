@@ -22,11 +22,12 @@ STATUS_NAMES = {
     0: "ATTN_OK", -1: "ATTN_ERR_NULL", -2: "ATTN_ERR_SHAPE", -3: "ATTN_ERR_GQA", -4: "ATTN_ERR_HEADDIM",
     -5: "ATTN_ERR_ALIGN", -6: "ATTN_ERR_CAUSAL_SQ_GT_SKV", -7: "ATTN_ERR_ARCH", -8: "ATTN_ERR_WORKSPACE",
     -9: "ATTN_ERR_LAUNCH", -10: "ATTN_ERR_DEVICE_TIMEOUT", -11: "ATTN_ERR_SCALE", -12: "ATTN_ERR_CUDA",
-    -13: "ATTN_ERR_SCRATCH_LIMIT",
+    -13: "ATTN_ERR_SCRATCH_LIMIT", -14: "ATTN_ERR_ROTATION", -15: "ATTN_ERR_EPS",
 }
 EXPORTED = ("attn_fwd", "attn_fwd_ex", "attn_fwd_host", "attn_fwd_strided", "attn_decode_ctas", "attn_status_string", "attn_version",
             "attn_device_status", "attn_decode_noalloc", "attn_decode_paged", "attn_prefill_paged", "attn_bwd", "attn_decode_fp8", "attn_prefill_fp8",
-            "attn_decode_paged_fp8", "attn_lse_merge")
+            "attn_decode_paged_fp8", "attn_lse_merge", "attn_qk_norm_rope", "attn_qk_norm_rope_bwd", "attn_append_paged",
+            "attn_append_paged_fp8")
 
 _lock = threading.Lock()
 _lib = None
@@ -81,6 +82,14 @@ def load_library(path: str | None = None):
         lib.attn_decode_paged_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, f, i, vp]
         lib.attn_lse_merge.restype = i
         lib.attn_lse_merge.argtypes = [vp, vp, vp, vp, vp, ctypes.c_longlong, i, vp]
+        lib.attn_qk_norm_rope.restype = i
+        lib.attn_qk_norm_rope.argtypes = [vp] * 9 + [i] * 5 + [ll3] * 4 + [i, i, i, f, vp]
+        lib.attn_qk_norm_rope_bwd.restype = i
+        lib.attn_qk_norm_rope_bwd.argtypes = [vp] * 14 + [i] * 5 + [ll3] * 6 + [i, i, i, f, vp]
+        lib.attn_append_paged.restype = i
+        lib.attn_append_paged.argtypes = [vp] * 14 + [i] * 4 + [ll3] * 4 + [i] * 6 + [f, vp]
+        lib.attn_append_paged_fp8.restype = i
+        lib.attn_append_paged_fp8.argtypes = [vp] * 16 + [i] * 4 + [ll3] * 4 + [i] * 6 + [f, vp]
         if path is None:
             _lib = lib
         return lib
@@ -488,6 +497,231 @@ def attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
                                      float(scale), int(bool(causal)), _stream_handle(stream))
     _check(rc)
     return dq, dk, dv
+
+
+_Strides = ctypes.c_longlong * 3
+_NORM_ROPE_BWD_BLOCKS = 592  # ATTN_QK_NORM_ROPE_BWD_WORKSPACE(D) holds two rows of D floats for each
+
+
+def _rows_strides(t):
+    return _Strides(*_strides3(t))
+
+
+def _same_device(first, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} must live on {first.device}, got {t.device}")
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _check_rotation(cos, sin, D):
+    """(rot_dim, max_pos) of the angle tables cos, sin [max_pos, rot_dim / 2]; (0, 0) without them."""
+    if cos is None and sin is None:
+        return 0, 0
+    _check_tensor("cos", cos, torch.float32, 2)
+    _check_tensor("sin", sin, torch.float32, 2)
+    if cos.shape != sin.shape:
+        raise ValueError(f"cos {tuple(cos.shape)} and sin {tuple(sin.shape)} must agree")
+    rot_dim = 2 * int(cos.shape[1])
+    if rot_dim > D:
+        raise ValueError(f"the tables rotate {rot_dim} channels of a head of {D}")
+    return rot_dim, int(cos.shape[0])
+
+
+def _check_weights(q_weight, k_weight, D):
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _check_tensor(name, w, torch.bfloat16, 1)
+            if w.shape[0] != D:
+                raise ValueError(f"{name} must be [{D}], got {tuple(w.shape)}")
+
+
+def _check_positions(positions, B, S):
+    if positions is not None:
+        _check_tensor("positions", positions, torch.int32, 2)
+        if tuple(positions.shape) != (B, S):
+            raise ValueError(f"positions must be [{B}, {S}], got {tuple(positions.shape)}")
+
+
+def _out_rows(name, t, like):
+    if t is None:
+        return torch.empty(like.shape, dtype=torch.bfloat16, device=like.device)
+    _check_rows(name, t, torch.bfloat16)
+    if t.shape != like.shape:
+        raise ValueError(f"{name} must have the shape {tuple(like.shape)}")
+    return t
+
+
+def attn_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor | None, sin: torch.Tensor | None,
+                      q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+                      positions: torch.Tensor | None = None, interleaved: bool = False, eps: float = 1e-6,
+                      q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None):
+    """Norm and rotation of queries and keys through ``attn_qk_norm_rope``: each head of each token is
+    RMS-normalised with a weight per channel (without weights: not) and its first 2 * cos.shape[1]
+    channels are rotated by the token's position.
+
+    q [B, Hq, S, D], k [B, Hkv, S, D] bf16, any view with a contiguous last axis (head slices of a fused
+    token-major projection, say); cos, sin fp32 [max_pos, rot_dim / 2], or None for both: no rotation;
+    q_weight, k_weight bf16 [D], both or neither; positions int32 [B, S] (default: the row index).
+    Returns (q_out, k_out), heads-major contiguous unless given; an output may be its input."""
+    _check_rows("q", q, torch.bfloat16)
+    _check_rows("k", k, torch.bfloat16)
+    B, Hq, S, D = q.shape
+    if k.shape[0] != B or k.shape[2] != S or k.shape[3] != D:
+        raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}")
+    rot_dim, max_pos = _check_rotation(cos, sin, D)
+    _check_weights(q_weight, k_weight, D)
+    _check_positions(positions, B, S)
+    q_out, k_out = _out_rows("q_out", q_out, q), _out_rows("k_out", k_out, k)
+    _same_device(q, k=k, cos=cos, sin=sin, q_weight=q_weight, k_weight=k_weight, positions=positions, q_out=q_out,
+                 k_out=k_out)
+    with torch.cuda.device(q.device):
+        rc = load_library().attn_qk_norm_rope(
+            q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(positions),
+            q_out.data_ptr(), k_out.data_ptr(), B, Hq, int(k.shape[1]), S, D, _rows_strides(q), _rows_strides(k),
+            _rows_strides(q_out), _rows_strides(k_out), rot_dim, max_pos, int(bool(interleaved)), float(eps),
+            _stream_handle(stream))
+    _check(rc)
+    return q_out, k_out
+
+
+def attn_qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor | None, sin: torch.Tensor | None,
+                          dq_out: torch.Tensor, dk_out: torch.Tensor, q_weight: torch.Tensor | None = None,
+                          k_weight: torch.Tensor | None = None, positions: torch.Tensor | None = None,
+                          interleaved: bool = False, eps: float = 1e-6, dq: torch.Tensor | None = None,
+                          dk: torch.Tensor | None = None, stream=None):
+    """Gradient of ``attn_qk_norm_rope`` through ``attn_qk_norm_rope_bwd``: dq_out, dk_out are the
+    gradients of its outputs (``attn_bwd``'s dq and dk), q, k and the rest its inputs. dq, dk may be
+    views (slices of a fused projection's gradient). Returns (dq, dk, dq_weight, dk_weight), the last
+    two fp32 [D], or None without weights."""
+    _check_rows("q", q, torch.bfloat16)
+    _check_rows("k", k, torch.bfloat16)
+    _check_rows("dq_out", dq_out, torch.bfloat16)
+    _check_rows("dk_out", dk_out, torch.bfloat16)
+    B, Hq, S, D = q.shape
+    if k.shape[0] != B or k.shape[2] != S or k.shape[3] != D or dq_out.shape != q.shape or dk_out.shape != k.shape:
+        raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}, dq_out {tuple(dq_out.shape)}, "
+                         f"dk_out {tuple(dk_out.shape)}")
+    rot_dim, max_pos = _check_rotation(cos, sin, D)
+    _check_weights(q_weight, k_weight, D)
+    _check_positions(positions, B, S)
+    dq, dk = _out_rows("dq", dq, q), _out_rows("dk", dk, k)
+    _same_device(q, k=k, cos=cos, sin=sin, dq_out=dq_out, dk_out=dk_out, q_weight=q_weight, k_weight=k_weight,
+                 positions=positions, dq=dq, dk=dk)
+    dwq = dwk = ws = None
+    with torch.cuda.device(q.device):
+        if q_weight is not None:
+            dwq, dwk = (torch.empty((D,), dtype=torch.float32, device=q.device) for _ in range(2))
+            # The caching allocator may hand this block out again once it is dropped: only behind the
+            # stream that uses it.
+            ws = torch.empty((_NORM_ROPE_BWD_BLOCKS * 2 * D,), dtype=torch.float32, device=q.device)
+            if stream is not None:
+                s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+                ws.record_stream(s)
+        rc = load_library().attn_qk_norm_rope_bwd(
+            q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(positions),
+            dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), _ptr(dwq), _ptr(dwk), _ptr(ws), B, Hq,
+            int(k.shape[1]), S, D, _rows_strides(q), _rows_strides(k), _rows_strides(dq_out), _rows_strides(dk_out),
+            _rows_strides(dq), _rows_strides(dk), rot_dim, max_pos, int(bool(interleaved)), float(eps),
+            _stream_handle(stream))
+    _check(rc)
+    return dq, dk, dwq, dwk
+
+
+def _append(k, v, cos, sin, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, q, q_out, q_weight, k_weight,
+            positions, new_lens, interleaved, eps, stream):
+    fp8 = k_scale is not None
+    _check_rows("k", k, torch.bfloat16)
+    _check_rows("v", v, torch.bfloat16)
+    if fp8:
+        k_pages, v_pages = _as_codes("k_pages", k_pages), _as_codes("v_pages", v_pages)
+    else:
+        _check_tensor("k_pages", k_pages, torch.bfloat16, 4)
+        _check_tensor("v_pages", v_pages, torch.bfloat16, 4)
+    _check_tensor("block_table", block_table, torch.int32, 2)
+    _check_tensor("seq_lens", seq_lens, torch.int32, 1)
+    B, Hkv, Sq, D = k.shape
+    num_pages, Hp, page_size, Dp = k_pages.shape
+    if v.shape != k.shape or v_pages.shape != k_pages.shape or Hp != Hkv or D != 128 or Dp != D:
+        raise ValueError(f"expected k, v [B,Hkv,Sq,128] and pages [P,Hkv,page,128]; got {tuple(k.shape)}, "
+                         f"{tuple(v.shape)}, {tuple(k_pages.shape)}, {tuple(v_pages.shape)}")
+    if block_table.shape[0] != B or seq_lens.shape[0] != B:
+        raise ValueError("block_table and seq_lens need one row / entry per batch element")
+    if new_lens is not None:
+        _check_tensor("new_lens", new_lens, torch.int32, 1)
+        if new_lens.shape[0] != B:
+            raise ValueError("new_lens needs one entry per batch element")
+    if fp8:
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            _check_tensor(name, t, torch.float32, 2)
+            if tuple(t.shape) != (Hkv, D):
+                raise ValueError(f"{name} must be [{Hkv}, {D}], got {tuple(t.shape)}")
+    rot_dim, max_pos = _check_rotation(cos, sin, D)
+    _check_weights(q_weight, k_weight, D)
+    _check_positions(positions, B, Sq)
+    Hq, qs, qos = 0, None, None
+    if q is not None:
+        _check_rows("q", q, torch.bfloat16)
+        if q.shape[0] != B or q.shape[2] != Sq or q.shape[3] != D:
+            raise ValueError(f"q must be [{B}, Hq, {Sq}, {D}], got {tuple(q.shape)}")
+        q_out = _out_rows("q_out", q_out, q)
+        Hq, qs, qos = int(q.shape[1]), _rows_strides(q), _rows_strides(q_out)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _same_device(k, v=v, q=q, q_out=q_out, cos=cos, sin=sin, k_pages=k_pages, v_pages=v_pages, k_scale=k_scale,
+                 v_scale=v_scale, block_table=block_table, seq_lens=seq_lens, new_lens=new_lens, positions=positions,
+                 q_weight=q_weight, k_weight=k_weight)
+    lib = load_library()
+    head = (_ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin),
+            _ptr(positions), seq_lens.data_ptr(), _ptr(new_lens), block_table.data_ptr(), _ptr(q_out),
+            k_pages.data_ptr(), v_pages.data_ptr())
+    with torch.cuda.device(k.device):
+        tail = (B, Hq, Hkv, Sq, qs, _rows_strides(k), _rows_strides(v), qos, num_pages, page_size,
+                int(block_table.shape[1]), rot_dim, max_pos, int(bool(interleaved)), float(eps),
+                _stream_handle(stream))
+        if fp8:
+            rc = lib.attn_append_paged_fp8(*head, k_scale.data_ptr(), v_scale.data_ptr(), *tail)
+        else:
+            rc = lib.attn_append_paged(*head, *tail)
+    _check(rc)
+    return q_out
+
+
+def attn_append_paged(k: torch.Tensor, v: torch.Tensor, cos: torch.Tensor | None, sin: torch.Tensor | None,
+                      k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                      q: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
+                      q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+                      positions: torch.Tensor | None = None, new_lens: torch.Tensor | None = None,
+                      interleaved: bool = False, eps: float = 1e-6, stream=None):
+    """Append new tokens to a paged cache through ``attn_append_paged``, keys normalised and rotated on
+    the way, and the queries too when given.
+
+    k, v [B, Hkv, Sq, 128] and q [B, Hq, Sq, 128] bf16, any view with a contiguous last axis; k_pages,
+    v_pages [num_pages, Hkv, page_size, 128] bf16, updated in place; block_table int32 [B,
+    pages_per_seq]; seq_lens int32 [B], counting the new tokens (what ``attn_decode_paged`` or
+    ``attn_prefill_paged`` takes next); new_lens int32 [B]: only the last new_lens[b] of the Sq rows are
+    tokens. The weights, tables and positions (default: the token's place in its sequence) as
+    ``attn_qk_norm_rope``. Returns q_out (None without q)."""
+    return _append(k, v, cos, sin, k_pages, v_pages, None, None, block_table, seq_lens, q, q_out, q_weight, k_weight,
+                   positions, new_lens, interleaved, eps, stream)
+
+
+def attn_append_paged_fp8(k: torch.Tensor, v: torch.Tensor, cos: torch.Tensor | None, sin: torch.Tensor | None,
+                          k_pages: torch.Tensor, v_pages: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                          block_table: torch.Tensor, seq_lens: torch.Tensor, q: torch.Tensor | None = None,
+                          q_out: torch.Tensor | None = None, q_weight: torch.Tensor | None = None,
+                          k_weight: torch.Tensor | None = None, positions: torch.Tensor | None = None,
+                          new_lens: torch.Tensor | None = None, interleaved: bool = False, eps: float = 1e-6,
+                          stream=None):
+    """``attn_append_paged`` to an e4m3 cache: pages hold codes (uint8 or float8_e4m3fn), k_scale, v_scale the cache's fp32
+    [Hkv, 128] coefficients; an element x is stored as the code nearest to x / coefficient."""
+    if k_scale is None or v_scale is None:
+        raise TypeError("k_scale and v_scale must be torch.Tensors")
+    return _append(k, v, cos, sin, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, q, q_out, q_weight,
+                   k_weight, positions, new_lens, interleaved, eps, stream)
 
 
 def decode_ctas(B: int, Hq: int, Hkv: int, Skv: int, D: int) -> int:

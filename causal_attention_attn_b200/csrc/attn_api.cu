@@ -265,6 +265,18 @@ int run(const void *q, const void *k, const void *v, void *o, float *lse, int B,
 }
 
 }  // namespace
+
+int check_device(int *sm_count)
+{
+    std::lock_guard<std::mutex> lock(g_mutex);
+    int err = ATTN_OK;
+    const DeviceState *s = device_state(&err);
+    if (!s)
+        return err;
+    *sm_count = s->sm_count;
+    return ATTN_OK;
+}
+
 }  // namespace attn_b200
 
 using namespace attn_b200;
@@ -505,6 +517,10 @@ extern "C" const char *attn_status_string(int status)
     case ATTN_ERR_SCRATCH_LIMIT:
         return "the decode needs more scratch than the fixed no-allocation buffer holds "
                "(too many (batch, kv head, head group) work units for attn_decode_noalloc)";
+    case ATTN_ERR_ROTATION:
+        return "rot_dim must be a multiple of 8 in [0, D], with cos and sin tables of max_pos >= 1 rows unless it is 0";
+    case ATTN_ERR_EPS:
+        return "eps must be finite and >= 0";
     default:
         return "unknown status";
     }

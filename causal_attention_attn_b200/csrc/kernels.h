@@ -106,6 +106,9 @@ struct DecodeArgs {
     const float *k_scale = nullptr, *v_scale = nullptr;
 };
 
+// ATTN_OK with the current device's SM count, or the attn_status that says why it cannot be used.
+int check_device(int *sm_count);
+
 // Returns a cudaError_t value (cudaSuccess on success); never synchronises.
 cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream, int *encode_error);
 
@@ -142,6 +145,43 @@ cudaError_t launch_bwd(const BwdArgs &a, cudaStream_t stream, int *encode_error)
 // (D in {32, 64, 128}); o_out (bf16, may be null) receives the merged O.
 cudaError_t launch_lse_merge(float *o_acc, float *lse_acc, const void *o_part, const float *lse_part, void *o_out,
                              long long rows, int D, int sm_count, cudaStream_t stream);
+
+// Norm and rotation of q and k (head dim 32, 64 or 128) and its gradient. Rows are the heads of the
+// B * S tokens; B * S * H stays below kMaxHeadRows, so that row numbers never pass 32 bits.
+constexpr long long kMaxHeadRows = 2147483647LL - 4096;
+constexpr int kNormRopeBwdBlocks = 592;  // blocks of the gradient at most: one partial of dw each
+struct NormRopeSide {
+    const void *x, *w, *dz;  // input, weight [D] (null: no norm), gradient of the output (backward)
+    void *out;               // the output, or the input's gradient
+    int H;
+    TensorStrides xs, zs, os;  // of x, dz and out
+};
+struct NormRopeArgs {
+    NormRopeSide q, k;
+    const float *cos, *sin;  // [max_pos][rot_dim / 2]
+    const int *positions;    // [B][S], or null: the row's index
+    int B, S, D, rot_dim, max_pos, interleaved;
+    float eps;
+    bool backward;
+    float *partials;   // backward with norm: [kNormRopeBwdBlocks][2][D], or null: no dw
+    float *dwq, *dwk;  // [D], either may be null
+};
+cudaError_t launch_norm_rope(const NormRopeArgs &a, cudaStream_t stream);
+
+// Append of B * S new tokens to a paged cache (head dim 128), keys normalised and rotated on the way,
+// queries too when given.
+struct AppendArgs {
+    const void *q, *k, *v;     // q may be null
+    const void *q_weight, *k_weight;
+    const float *cos, *sin;
+    const int *positions, *seq_lens, *new_lens, *block_table;  // positions, new_lens may be null
+    void *q_out, *k_pages, *v_pages;
+    const float *k_scale, *v_scale;  // e4m3 cache: [Hkv][128]; null: bf16 cache
+    int B, Hq, Hkv, S, num_pages, page_size, pages_per_seq, rot_dim, max_pos, interleaved;
+    float eps;
+    TensorStrides qs, ks, vs, qos;
+};
+cudaError_t launch_append(const AppendArgs &a, cudaStream_t stream);
 
 // Decode planning and launch. requested_ctas <= 0 means one CTA per resident slot on the device.
 int decode_heads_per_cta(int group, int D);  // G: 1, 2, 4 or 8 (up to 16 for D = 128)

@@ -59,7 +59,9 @@ typedef enum attn_status {
     ATTN_ERR_DEVICE_TIMEOUT = -10,  /* a kernel-side wait ran out (reported by attn_device_status) */
     ATTN_ERR_SCALE = -11,           /* scale is not finite and > 0 */
     ATTN_ERR_CUDA = -12,            /* a CUDA runtime call failed (device query, tensor map, copy) */
-    ATTN_ERR_SCRATCH_LIMIT = -13    /* attn_decode_noalloc: the problem needs more scratch than its fixed buffer */
+    ATTN_ERR_SCRATCH_LIMIT = -13,   /* attn_decode_noalloc: the problem needs more scratch than its fixed buffer */
+    ATTN_ERR_ROTATION = -14,        /* rot_dim is not a multiple of 8 in [0, D], or its tables have no row */
+    ATTN_ERR_EPS = -15              /* eps is not finite and >= 0 */
 } attn_status;
 
 /*
@@ -346,6 +348,118 @@ int attn_decode_paged_fp8(const void *q, const void *k_pages, const void *v_page
  */
 int attn_lse_merge(float *o_acc, float *lse_acc, const void *o_part, const float *lse_part, void *o_out,
                    long long rows, int D, void *stream);
+
+/*
+ * attn_qk_norm_rope — the queries and keys of one layer made ready for attention: each head of each
+ * token normalised (RMS, a weight per channel) and rotated by its position, in one pass.
+ *
+ * Per row x (one head of one token, D elements), with w = q_weight or k_weight, pos the token's
+ * position, R = rot_dim:
+ *   y = x / sqrt(mean(x^2) + eps) * w                 (no weights given: y = x)
+ *   z_a = y_a c - y_b s,  z_b = y_b c + y_a s         for each pair (a, b) of channels j < R / 2,
+ *   z_d = y_d                                         for d >= R,
+ * c = cos[pos][j], s = sin[pos][j]; pair j is channels (j, j + R / 2), or (2j, 2j + 1) when
+ * `interleaved`. Computed in fp32 and rounded to bf16 once.
+ *
+ * Source (page title, section): the RMS norm — "AI Infra 入门：RMSNorm、Softmax、Causal Mask、Sampling
+ * 的数学与底层优化", its RMSNorm section; the rotation is an interface addition: the pages' attention
+ * takes q and k as they come.
+ *
+ *   q, k             bf16 [B, Hq, S, D] and [B, Hkv, S, D] with element strides {batch, head, row}
+ *                    q_strides, k_strides (host arrays; a contiguous D; the rule of
+ *                    attn_fwd_strided), e.g. head slices of a fused token-major projection.
+ *   q_out, k_out     likewise, with their own strides; attn_fwd and attn_bwd want the contiguous
+ *                    [B, H, S, D]. The output may be the input itself (same pointer and strides);
+ *                    they must not overlap in another way.
+ *   q_weight,        bf16 [D], shared by all heads; both, or NULL for both: no norm.
+ *   k_weight
+ *   cos, sin         fp32 [max_pos, rot_dim / 2]; NULL only when rot_dim is 0.
+ *   positions        int32 [B, S] on the device, or NULL: row i of every batch entry is at position
+ *                    i. A position outside [0, max_pos) reads no table: that token's rows of q_out
+ *                    and k_out are zeros (unless rot_dim is 0, when positions are not looked at).
+ *   D                32, 64 or 128. rot_dim: a multiple of 8 in [0, D].
+ *   eps              finite and >= 0.
+ * Hq and Hkv need not divide one another here. Pointers 16-byte aligned (positions: 4). Never
+ * allocates or synchronises; returns ATTN_OK or a negative attn_status (before any launch).
+ */
+int attn_qk_norm_rope(const void *q, const void *k, const void *q_weight, const void *k_weight, const float *cos,
+                      const float *sin, const int *positions, void *q_out, void *k_out, int B, int Hq, int Hkv, int S,
+                      int D, const long long *q_strides, const long long *k_strides, const long long *q_out_strides,
+                      const long long *k_out_strides, int rot_dim, int max_pos, int interleaved, float eps,
+                      void *stream);
+
+/*
+ * attn_qk_norm_rope_bwd — the gradient of attn_qk_norm_rope: given dq_out = dL/dq_out and dk_out,
+ *   per row: dy = the rotation's transpose of dz, g = w dy, r = (mean(x^2) + eps)^(-1/2),
+ *            dx = r (g - x r^2 mean(g x));   dq_weight, dk_weight = sum over all rows of dy x r.
+ *   q, k, the weights, cos, sin, positions   as given to the forward call (its inputs, not outputs).
+ *   dq_out, dk_out        bf16, with their own strides, e.g. the dq and dk of attn_bwd.
+ *   dq, dk                bf16, with their own strides (slices of a fused projection's gradient, say).
+ *                         Each may be dq_out / dk_out or q / k itself (same pointer and strides).
+ *   dq_weight, dk_weight  fp32 [D], or NULL where not wanted (must be NULL without weights). Summed in
+ *                         fp32 in a fixed order: the same call gives the same bits.
+ *   workspace             ATTN_QK_NORM_ROPE_BWD_WORKSPACE(D) bytes on the device, 16-byte aligned,
+ *                         owned by the caller and used only until the call's work is done; may be NULL
+ *                         when neither weight gradient is wanted. Calls that overlap need one each.
+ * A token whose position has no row of the tables has zero gradients. Without weights q and k may
+ * be NULL. Other arguments, rules and errors as attn_qk_norm_rope.
+ */
+#define ATTN_QK_NORM_ROPE_BWD_WORKSPACE(D) (592u * 2u * 4u * (unsigned)(D))
+int attn_qk_norm_rope_bwd(const void *q, const void *k, const void *q_weight, const void *k_weight, const float *cos,
+                          const float *sin, const int *positions, const void *dq_out, const void *dk_out, void *dq,
+                          void *dk, float *dq_weight, float *dk_weight, void *workspace, int B, int Hq, int Hkv, int S,
+                          int D, const long long *q_strides, const long long *k_strides,
+                          const long long *dq_out_strides, const long long *dk_out_strides,
+                          const long long *dq_strides, const long long *dk_strides, int rot_dim, int max_pos,
+                          int interleaved, float eps, void *stream);
+
+/*
+ * attn_append_paged — the step before attn_decode_paged or attn_prefill_paged: Sq new tokens of each
+ * sequence written to the paged cache, their keys normalised and rotated on the way (the arithmetic
+ * of attn_qk_norm_rope, D = 128), and, when given, their queries too.
+ *
+ * Source (page title, section): the cache grows by the new tokens' keys and values — "第11节：Attention
+ * 实现（Flash vs Fallback）", §3 and "Bộ 06 · Bên trong model", Q2. The page layout is attn_decode_paged's.
+ *
+ *   k, v          bf16 [B, Hkv, Sq, 128] with element strides {batch, head, row}, as attn_qk_norm_rope.
+ *   q, q_out      bf16 [B, Hq, Sq, 128] with their strides, or NULL for both (Hq = 0). q_out may be q
+ *                 itself (same pointer and strides).
+ *   seq_lens      int32 [B]: the sequences' lengths WITH the new tokens, as the attention call that
+ *                 follows takes them: row i of sequence b is its token seq_lens[b] - Sq + i.
+ *   new_lens      int32 [B], or NULL: only the last new_lens[b] (clamped to [0, Sq]) of sequence b's Sq
+ *                 rows are tokens; the rows before them are padding. NULL: all Sq are.
+ *   positions     int32 [B, Sq], or NULL: a token's rotation position is its place in the sequence. For
+ *                 suffixes behind a shared prefix (attn_decode_prefix) give prefix + place.
+ *   k_pages, v_pages, block_table, num_pages, page_size, pages_per_seq   as attn_decode_paged.
+ *   q_weight, k_weight, cos, sin, rot_dim, max_pos, interleaved, eps     as attn_qk_norm_rope; without
+ *                 q, k_weight alone chooses the norm.
+ * A row is left out when it is padding, when its place lies outside [0, pages_per_seq * page_size),
+ * when its block-table entry lies outside [0, num_pages), or (rot_dim > 0) its position outside
+ * [0, max_pos): nothing of the cache changes for it, and its q_out rows are zeros. Every other slot of
+ * the cache stays as it was. Two tokens of one call that name the same slot leave either one's row.
+ * Lengths are read on the device. Never allocates or synchronises; errors as the calls above.
+ */
+int attn_append_paged(const void *q, const void *k, const void *v, const void *q_weight, const void *k_weight,
+                      const float *cos, const float *sin, const int *positions, const int *seq_lens,
+                      const int *new_lens, const int *block_table, void *q_out, void *k_pages, void *v_pages, int B,
+                      int Hq, int Hkv, int Sq, const long long *q_strides, const long long *k_strides,
+                      const long long *v_strides, const long long *q_out_strides, int num_pages, int page_size,
+                      int pages_per_seq, int rot_dim, int max_pos, int interleaved, float eps, void *stream);
+
+/*
+ * attn_append_paged_fp8 — attn_append_paged to an e4m3 cache (attn_decode_paged_fp8's): the stored
+ * code of a key or value element x of kv head g, channel d is the e4m3 value nearest to
+ * x / k_scale[g, d] (v_scale), ties to even, magnitudes above 448 stored as 448, NaN as NaN; x is the
+ * fp32 value, not rounded to bf16 first. k_scale, v_scale: fp32 [Hkv, 128], the cache's coefficients.
+ * Every other argument and rule is attn_append_paged's.
+ */
+int attn_append_paged_fp8(const void *q, const void *k, const void *v, const void *q_weight, const void *k_weight,
+                          const float *cos, const float *sin, const int *positions, const int *seq_lens,
+                          const int *new_lens, const int *block_table, void *q_out, void *k_pages, void *v_pages,
+                          const float *k_scale, const float *v_scale, int B, int Hq, int Hkv, int Sq,
+                          const long long *q_strides, const long long *k_strides, const long long *v_strides,
+                          const long long *q_out_strides, int num_pages, int page_size, int pages_per_seq, int rot_dim,
+                          int max_pos, int interleaved, float eps, void *stream);
 
 #ifdef __cplusplus
 }
