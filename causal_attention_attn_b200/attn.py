@@ -8,6 +8,7 @@ in the library's kernels. There is no fallback: if the library is missing the ca
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -499,18 +500,47 @@ def attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
     return dq, dk, dv
 
 
-_Strides = ctypes.c_longlong * 3
 _NORM_ROPE_BWD_BLOCKS = 592  # ATTN_QK_NORM_ROPE_BWD_WORKSPACE(D) holds two rows of D floats for each
 
+# The calls below come once per layer and token, so the host's time counts: a call's tensors are
+# checked with as few torch calls as the checks need.
 
-def _rows_strides(t):
-    return _Strides(*_strides3(t))
+
+@functools.lru_cache(maxsize=1024)
+def _stride_array(b: int, h: int, s: int):
+    """The {batch, head, row} array the library reads strides from (read only, so calls share it)."""
+    return (ctypes.c_longlong * 3)(b, h, s)
 
 
-def _same_device(first, **tensors):
+def _rows_strides(t, shape):
+    """As ``_strides3`` of a [B, H, S, D] tensor whose shape is at hand."""
+    b, h, s, _ = t.stride()
+    B, H, S, D = shape
+    return _stride_array(b if B > 1 else D, h if H > 1 else D, s if S > 1 else D)
+
+
+def _same_device(index, **tensors):
     for name, t in tensors.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} must live on {first.device}, got {t.device}")
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{name} must live on cuda:{index}, got {t.device}")
+
+
+class _Launch:
+    """The device of a call's tensors made current for the call (when it is not), and the stream."""
+    __slots__ = ("guard", "handle")
+
+    def __init__(self, index, stream):
+        self.handle = _stream_handle(torch.cuda.current_stream(index) if stream is None else stream)
+        self.guard = None if torch.cuda.current_device() == index else torch.cuda.device(index)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
 
 
 def _ptr(t):
@@ -523,12 +553,12 @@ def _check_rotation(cos, sin, D):
         return 0, 0
     _check_tensor("cos", cos, torch.float32, 2)
     _check_tensor("sin", sin, torch.float32, 2)
-    if cos.shape != sin.shape:
+    max_pos, half = shape = cos.shape
+    if sin.shape != shape:
         raise ValueError(f"cos {tuple(cos.shape)} and sin {tuple(sin.shape)} must agree")
-    rot_dim = 2 * int(cos.shape[1])
-    if rot_dim > D:
-        raise ValueError(f"the tables rotate {rot_dim} channels of a head of {D}")
-    return rot_dim, int(cos.shape[0])
+    if 2 * half > D:
+        raise ValueError(f"the tables rotate {2 * half} channels of a head of {D}")
+    return 2 * half, max_pos
 
 
 def _check_weights(q_weight, k_weight, D):
@@ -569,21 +599,23 @@ def attn_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor | None
     Returns (q_out, k_out), heads-major contiguous unless given; an output may be its input."""
     _check_rows("q", q, torch.bfloat16)
     _check_rows("k", k, torch.bfloat16)
-    B, Hq, S, D = q.shape
-    if k.shape[0] != B or k.shape[2] != S or k.shape[3] != D:
+    B, Hq, S, D = qshape = q.shape
+    Bk, Hkv, Sk, Dk = kshape = k.shape
+    if Bk != B or Sk != S or Dk != D:
         raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}")
     rot_dim, max_pos = _check_rotation(cos, sin, D)
     _check_weights(q_weight, k_weight, D)
     _check_positions(positions, B, S)
     q_out, k_out = _out_rows("q_out", q_out, q), _out_rows("k_out", k_out, k)
-    _same_device(q, k=k, cos=cos, sin=sin, q_weight=q_weight, k_weight=k_weight, positions=positions, q_out=q_out,
+    dev = q.get_device()
+    _same_device(dev, k=k, cos=cos, sin=sin, q_weight=q_weight, k_weight=k_weight, positions=positions, q_out=q_out,
                  k_out=k_out)
-    with torch.cuda.device(q.device):
+    with _Launch(dev, stream) as handle:
         rc = load_library().attn_qk_norm_rope(
             q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(positions),
-            q_out.data_ptr(), k_out.data_ptr(), B, Hq, int(k.shape[1]), S, D, _rows_strides(q), _rows_strides(k),
-            _rows_strides(q_out), _rows_strides(k_out), rot_dim, max_pos, int(bool(interleaved)), float(eps),
-            _stream_handle(stream))
+            q_out.data_ptr(), k_out.data_ptr(), B, Hq, Hkv, S, D, _rows_strides(q, qshape), _rows_strides(k, kshape),
+            _rows_strides(q_out, qshape), _rows_strides(k_out, kshape), rot_dim, max_pos, 1 if interleaved else 0, eps,
+            handle)
     _check(rc)
     return q_out, k_out
 
@@ -601,32 +633,35 @@ def attn_qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor | 
     _check_rows("k", k, torch.bfloat16)
     _check_rows("dq_out", dq_out, torch.bfloat16)
     _check_rows("dk_out", dk_out, torch.bfloat16)
-    B, Hq, S, D = q.shape
-    if k.shape[0] != B or k.shape[2] != S or k.shape[3] != D or dq_out.shape != q.shape or dk_out.shape != k.shape:
+    B, Hq, S, D = qshape = q.shape
+    Bk, Hkv, Sk, Dk = kshape = k.shape
+    if Bk != B or Sk != S or Dk != D or dq_out.shape != qshape or dk_out.shape != kshape:
         raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}, dq_out {tuple(dq_out.shape)}, "
                          f"dk_out {tuple(dk_out.shape)}")
     rot_dim, max_pos = _check_rotation(cos, sin, D)
     _check_weights(q_weight, k_weight, D)
     _check_positions(positions, B, S)
     dq, dk = _out_rows("dq", dq, q), _out_rows("dk", dk, k)
-    _same_device(q, k=k, cos=cos, sin=sin, dq_out=dq_out, dk_out=dk_out, q_weight=q_weight, k_weight=k_weight,
+    dev = q.get_device()
+    _same_device(dev, k=k, cos=cos, sin=sin, dq_out=dq_out, dk_out=dk_out, q_weight=q_weight, k_weight=k_weight,
                  positions=positions, dq=dq, dk=dk)
     dwq = dwk = ws = None
-    with torch.cuda.device(q.device):
+    with _Launch(dev, stream) as handle:
         if q_weight is not None:
-            dwq, dwk = (torch.empty((D,), dtype=torch.float32, device=q.device) for _ in range(2))
-            # The caching allocator may hand this block out again once it is dropped: only behind the
-            # stream that uses it.
+            # One block for the weights' gradients (two views of 16-byte aligned rows) and one that the
+            # kernels use and nobody else: the caching allocator hands it out again behind this stream.
+            dwq, dwk = torch.empty((2, D), dtype=torch.float32, device=q.device).unbind(0)
             ws = torch.empty((_NORM_ROPE_BWD_BLOCKS * 2 * D,), dtype=torch.float32, device=q.device)
             if stream is not None:
-                s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
-                ws.record_stream(s)
+                used = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+                for t in (dwq, ws):
+                    t.record_stream(used)
         rc = load_library().attn_qk_norm_rope_bwd(
             q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(positions),
             dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), _ptr(dwq), _ptr(dwk), _ptr(ws), B, Hq,
-            int(k.shape[1]), S, D, _rows_strides(q), _rows_strides(k), _rows_strides(dq_out), _rows_strides(dk_out),
-            _rows_strides(dq), _rows_strides(dk), rot_dim, max_pos, int(bool(interleaved)), float(eps),
-            _stream_handle(stream))
+            Hkv, S, D, _rows_strides(q, qshape), _rows_strides(k, kshape), _rows_strides(dq_out, qshape),
+            _rows_strides(dk_out, kshape), _rows_strides(dq, qshape), _rows_strides(dk, kshape), rot_dim, max_pos,
+            1 if interleaved else 0, eps, handle)
     _check(rc)
     return dq, dk, dwq, dwk
 
@@ -643,12 +678,13 @@ def _append(k, v, cos, sin, k_pages, v_pages, k_scale, v_scale, block_table, seq
         _check_tensor("v_pages", v_pages, torch.bfloat16, 4)
     _check_tensor("block_table", block_table, torch.int32, 2)
     _check_tensor("seq_lens", seq_lens, torch.int32, 1)
-    B, Hkv, Sq, D = k.shape
-    num_pages, Hp, page_size, Dp = k_pages.shape
-    if v.shape != k.shape or v_pages.shape != k_pages.shape or Hp != Hkv or D != 128 or Dp != D:
+    B, Hkv, Sq, D = shape = k.shape
+    num_pages, Hp, page_size, Dp = pages = k_pages.shape
+    if v.shape != shape or v_pages.shape != pages or Hp != Hkv or D != 128 or Dp != D:
         raise ValueError(f"expected k, v [B,Hkv,Sq,128] and pages [P,Hkv,page,128]; got {tuple(k.shape)}, "
                          f"{tuple(v.shape)}, {tuple(k_pages.shape)}, {tuple(v_pages.shape)}")
-    if block_table.shape[0] != B or seq_lens.shape[0] != B:
+    rows, per_seq = block_table.shape
+    if rows != B or seq_lens.shape[0] != B:
         raise ValueError("block_table and seq_lens need one row / entry per batch element")
     if new_lens is not None:
         _check_tensor("new_lens", new_lens, torch.int32, 1)
@@ -665,23 +701,24 @@ def _append(k, v, cos, sin, k_pages, v_pages, k_scale, v_scale, block_table, seq
     Hq, qs, qos = 0, None, None
     if q is not None:
         _check_rows("q", q, torch.bfloat16)
-        if q.shape[0] != B or q.shape[2] != Sq or q.shape[3] != D:
+        Bq, Hq, S, Dq = qshape = q.shape
+        if Bq != B or S != Sq or Dq != D:
             raise ValueError(f"q must be [{B}, Hq, {Sq}, {D}], got {tuple(q.shape)}")
         q_out = _out_rows("q_out", q_out, q)
-        Hq, qs, qos = int(q.shape[1]), _rows_strides(q), _rows_strides(q_out)
+        qs, qos = _rows_strides(q, qshape), _rows_strides(q_out, qshape)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _same_device(k, v=v, q=q, q_out=q_out, cos=cos, sin=sin, k_pages=k_pages, v_pages=v_pages, k_scale=k_scale,
+    dev = k.get_device()
+    _same_device(dev, v=v, q=q, q_out=q_out, cos=cos, sin=sin, k_pages=k_pages, v_pages=v_pages, k_scale=k_scale,
                  v_scale=v_scale, block_table=block_table, seq_lens=seq_lens, new_lens=new_lens, positions=positions,
                  q_weight=q_weight, k_weight=k_weight)
     lib = load_library()
     head = (_ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin),
             _ptr(positions), seq_lens.data_ptr(), _ptr(new_lens), block_table.data_ptr(), _ptr(q_out),
             k_pages.data_ptr(), v_pages.data_ptr())
-    with torch.cuda.device(k.device):
-        tail = (B, Hq, Hkv, Sq, qs, _rows_strides(k), _rows_strides(v), qos, num_pages, page_size,
-                int(block_table.shape[1]), rot_dim, max_pos, int(bool(interleaved)), float(eps),
-                _stream_handle(stream))
+    with _Launch(dev, stream) as handle:
+        tail = (B, Hq, Hkv, Sq, qs, _rows_strides(k, shape), _rows_strides(v, shape), qos, num_pages, page_size,
+                per_seq, rot_dim, max_pos, 1 if interleaved else 0, eps, handle)
         if fp8:
             rc = lib.attn_append_paged_fp8(*head, k_scale.data_ptr(), v_scale.data_ptr(), *tail)
         else:

@@ -9,8 +9,9 @@
  * is rounded once, not to bf16 first.
  *
  * Bound by memory (each new row read and written once), and for a few tokens by the launch and one
- * chain of dependent loads: length, block-table entry, store. The rows of the inputs are loaded
- * before the chain's results are needed.
+ * chain of dependent loads: length, block-table entry and angles, store. The persistent blocks and
+ * their rings are norm_rope_sm100.cu's; a unit's length and block-table entry are looked up when its
+ * rows are sent for.
  */
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -31,12 +32,12 @@ using R = RowLanes<kD>;
 
 enum Kind : int { kQ = 0, kK = 1, kV = 2 };
 
-// The rows of q, k or v, numbered token * H + head, token = b * S + i.
+// One of q, k and v, in pairs of neighbouring heads of one token (as in norm_rope_sm100.cu).
 struct Source {
     const __nv_bfloat16 *x, *w;
     TensorStrides xs;
-    FastDiv heads;
-    int rows, units;
+    FastDiv pairs_per_token;
+    int heads, pairs, units;
 };
 
 struct AppendParams {
@@ -53,6 +54,11 @@ struct AppendParams {
     float eps;
 };
 
+constexpr int kStages = 3;
+constexpr int kAngles = 2 * kRowSlots;  // a stage: two rows, then the angles
+constexpr int kStageBytes = (kAngles + kAngleSlots) * kSlotBytes;
+constexpr int kSmem = kWarps * kStages * kStageBytes;
+
 // Four consecutive elements' e4m3 codes, the first in the low byte.
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
 {
@@ -61,123 +67,136 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
     return lo | (hi << 16);
 }
 
-template <bool kInterleaved, bool kFp8, int kIter>
-__global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p)
+template <bool kInterleaved, bool kFp8>
+__global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendParams p)
 {
-    const int lane = threadIdx.x & 31;
-    const int l = lane & (R::kLanes - 1);
-    int unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
-    int kind = kQ;
-    while (kind <= kV && unit >= p.src[kind].units) {
-        unit -= p.src[kind].units;
-        ++kind;
-    }
-    if (kind > kV)
-        return;
-    const Source &sc = p.src[kind];
-    const int row0 = unit * (R::kRows * kIter) + lane / R::kLanes;
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int l = lane & (R::kLanes - 1), group = lane / R::kLanes;
     const LaneElems le = lane_elems<kInterleaved>(l, p.table.rot);
+    const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(warp * kStages * kStageBytes + lane * 16);
+    const int n_q = p.src[kQ].units, n_qk = n_q + p.src[kK].units, n_units = n_qk + p.src[kV].units;
+    const int step = gridDim.x * kWarps, first = blockIdx.x * kWarps + warp;
+    auto kind_of = [&](int unit) { return unit < n_q ? kQ : unit < n_qk ? kK : kV; };
 
     struct At {
-        bool row, live;  // a row of the input; of a token that is appended
-        uint32_t b, i, h;
-        long long pos;  // the token's slot in its sequence
-        int rot_pos, page;
-    } at[kIter];
-    uint2 g0[kIter], g1[kIter];
-    float4 c[kIter], s[kIter];
-#pragma unroll
-    for (int k = 0; k < kIter; ++k) {
-        const int row = row0 + k * R::kRows;
-        At &a = at[k];
-        a.row = row < sc.rows;
-        const uint32_t n = a.row ? static_cast<uint32_t>(row) : 0u;
-        const uint32_t tok = sc.heads.quot(n);
-        a.h = n - tok * sc.heads.d;
-        a.b = p.seq.quot(tok);
-        a.i = tok - a.b * p.seq.d;
-        const __nv_bfloat16 *x = sc.x + a.b * sc.xs.b + a.h * sc.xs.h + a.i * sc.xs.s;
-        g0[k] = g1[k] = make_uint2(0u, 0u);
-        if (a.row) {
-            g0[k] = *reinterpret_cast<const uint2 *>(x + le.e0);
-            g1[k] = *reinterpret_cast<const uint2 *>(x + le.e1);
-        }
-        const long long S = p.seq.d;
-        const long long fresh = p.new_lens ? min(max(static_cast<long long>(__ldg(p.new_lens + a.b)), 0LL), S) : S;
-        a.pos = static_cast<long long>(__ldg(p.seq_lens + a.b)) - S + a.i;
-        a.live = a.row && a.i >= S - fresh && a.pos >= 0 && a.pos < p.cap;
-        a.rot_pos = p.positions ? __ldg(p.positions + tok) : static_cast<int>(a.live ? a.pos : 0);
-        a.live = a.live && (p.table.rot == 0 || (a.rot_pos >= 0 && a.rot_pos < p.table.max_pos));
-    }
-#pragma unroll
-    for (int k = 0; k < kIter; ++k) {
-        At &a = at[k];
-        a.page = -1;
-        if (a.live)
-            a.page = __ldg(p.block_table + static_cast<size_t>(a.b) * p.pages_per_seq +
-                           p.page_size.quot(static_cast<uint32_t>(a.pos)));
-        load_angles(p.table, a.rot_pos, l, kind != kV && le.rotated && a.live, c[k], s[k]);
-    }
-    const bool norm = sc.w != nullptr;
-    Pairs w;
-    if (norm)
-        w = load_weight<kInterleaved>(sc.w, le);
-#pragma unroll
-    for (int k = 0; k < kIter; ++k) {
-        At &a = at[k];
-        a.live = a.live && a.page >= 0 && a.page < p.num_pages;
-        Pairs x = unpack_pairs<kInterleaved>(g0[k], g1[k]);
-        if (norm) {
-            const float r = rsqrtf(row_sum<kD>(pairs_dot(x, x)) * (1.f / kD) + p.eps);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                x.A[u] *= r * w.A[u];
-                x.B[u] *= r * w.B[u];
+        bool live0, live1;  // the pair's rows exist
+        bool token;         // their token has a slot and a position
+        uint32_t b, i, h, slot;
+        int page;
+    } at[kStages];
+    auto issue = [&](int unit, int s) {
+        if (unit < n_units) {
+            const Kind kind = kind_of(unit);
+            const Source &sc = p.src[kind];
+            At &a = at[s];
+            const int pair = (unit - (kind == kQ ? 0 : kind == kK ? n_q : n_qk)) * R::kRows + group;
+            a.live0 = pair < sc.pairs;
+            const uint32_t n = a.live0 ? static_cast<uint32_t>(pair) : 0u;
+            const uint32_t tok = sc.pairs_per_token.quot(n);
+            a.h = 2 * (n - tok * sc.pairs_per_token.d);
+            a.live1 = a.live0 && static_cast<int>(a.h) + 1 < sc.heads;
+            a.b = p.seq.quot(tok);
+            a.i = tok - a.b * p.seq.d;
+            const uint32_t base = ring + static_cast<uint32_t>(s * kStageBytes);
+            const __nv_bfloat16 *x = sc.x + (a.b * sc.xs.b + a.h * sc.xs.h + a.i * sc.xs.s);
+            copy_row(base, x, le, a.live0);
+            copy_row(base + kRowSlots * kSlotBytes, a.live1 ? x + sc.xs.h : x, le, a.live1);
+            const long long S = p.seq.d;
+            const long long fresh = p.new_lens ? min(max(static_cast<long long>(__ldg(p.new_lens + a.b)), 0LL), S) : S;
+            const long long place = static_cast<long long>(__ldg(p.seq_lens + a.b)) - S + a.i;
+            a.token = a.live0 && a.i >= S - fresh && place >= 0 && place < p.cap;
+            const int pos = p.positions ? __ldg(p.positions + tok) : static_cast<int>(a.token ? place : 0);
+            a.token = a.token && p.table.has(pos);
+            a.page = -1;
+            a.slot = 0;
+            if (a.token) {
+                const uint32_t e = p.page_size.quot(static_cast<uint32_t>(place));
+                a.slot = static_cast<uint32_t>(place) - e * p.page_size.d;
+                a.page = __ldg(p.block_table + static_cast<size_t>(a.b) * p.pages_per_seq + e);
+                if (kind != kV && le.rotated)
+                    copy_angles(base + kAngles * kSlotBytes, p.table, pos, l);
             }
         }
-        if (kind != kV && le.rotated)
-            rotate_pairs(x, c[k], s[k]);
-        uint2 o0, o1;
-        pack_pairs<kInterleaved>(x, o0, o1);
-        if (kind == kQ) {
-            if (a.row) {
-                __nv_bfloat16 *out = p.q_out + a.b * p.qos.b + a.h * p.qos.h + a.i * p.qos.s;
-                const uint2 zero = make_uint2(0u, 0u);
-                *reinterpret_cast<uint2 *>(out + le.e0) = a.live ? o0 : zero;
-                *reinterpret_cast<uint2 *>(out + le.e1) = a.live ? o1 : zero;
-            }
-            continue;
-        }
-        if (!a.live)
-            continue;
-        const uint32_t slot = static_cast<uint32_t>(a.pos) - p.page_size.quot(static_cast<uint32_t>(a.pos)) * p.page_size.d;
-        const size_t dst = ((static_cast<size_t>(a.page) * p.Hkv + a.h) * p.page_size.d + slot) * kD;
-        if constexpr (kFp8) {
-            const float *cf = p.coef[kind - kK] + a.h * kD;
-            const Pairs f = arrange_pairs<kInterleaved>(__ldg(reinterpret_cast<const float4 *>(cf + le.e0)),
-                                                        __ldg(reinterpret_cast<const float4 *>(cf + le.e1)));
+        copy_commit();
+    };
+
+    auto consume = [&](int unit, int s) {
+        const Kind kind = kind_of(unit);
+        const Source &sc = p.src[kind];
+        const uint32_t base = ring + static_cast<uint32_t>(s * kStageBytes);
+        const At a = at[s];
+        const bool write = a.token && a.page >= 0 && a.page < p.num_pages;
+        const bool norm = sc.w != nullptr, turn = kind != kV && le.rotated && a.token;
+        Angles ang;
+        if (turn)
+            ang = read_angles(base + kAngles * kSlotBytes);
+        const RawRow wraw = norm ? load_row(sc.w, le) : zero_row();
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                x.A[u] = x.A[u] / f.A[u];
-                x.B[u] = x.B[u] / f.B[u];
+        for (int k = 0; k < 2; ++k) {
+            const bool live = k ? a.live1 : a.live0;
+            const uint32_t h = a.h + k;
+            Pairs x = unpack_pairs<kInterleaved>(read_row(base + k * kRowSlots * kSlotBytes));
+            if (norm) {
+                const Pairs w = unpack_pairs<kInterleaved>(wraw);
+                const float r = rsqrtf(row_sum<kD>(pairs_dot(x, x)) * (1.f / kD) + p.eps);
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    x.A[u] *= r * w.A[u];
+                    x.B[u] *= r * w.B[u];
+                }
             }
-            uint8_t *out = static_cast<uint8_t *>(p.pages[kind - kK]) + dst;
-            uint32_t w0, w1;
-            if constexpr (kInterleaved) {
-                w0 = e4m3x4(x.A[0], x.B[0], x.A[1], x.B[1]);
-                w1 = e4m3x4(x.A[2], x.B[2], x.A[3], x.B[3]);
+            if (turn)
+                rotate_pairs<false>(x, ang);
+            if (kind == kQ) {
+                if (live)
+                    store_row(p.q_out + (a.b * p.qos.b + h * p.qos.h + a.i * p.qos.s), le,
+                              write ? pack_pairs<kInterleaved>(x) : zero_row());
+                continue;
+            }
+            if (!write || !live)
+                continue;
+            const size_t dst = ((static_cast<size_t>(a.page) * p.Hkv + h) * p.page_size.d + a.slot) * kD;
+            if constexpr (kFp8) {
+                const float *cf = p.coef[kind - kK] + h * kD;
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {  // four elements at a time, in element order
+                    const float4 f = __ldg(reinterpret_cast<const float4 *>(cf + (j < 2 ? le.e0 : le.e1) + 4 * (j & 1)));
+                    float v[4];
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const int e = 4 * j + t;  // of the lane's sixteen
+                        v[t] = kInterleaved ? ((e & 1) ? x.B[e >> 1] : x.A[e >> 1]) : (e < 8 ? x.A[e & 7] : x.B[e & 7]);
+                    }
+                    w[j] = e4m3x4(v[0] / f.x, v[1] / f.y, v[2] / f.z, v[3] / f.w);
+                }
+                uint8_t *out = static_cast<uint8_t *>(p.pages[kind - kK]) + dst;
+                *reinterpret_cast<uint2 *>(out + le.e0) = make_uint2(w[0], w[1]);
+                *reinterpret_cast<uint2 *>(out + le.e1) = make_uint2(w[2], w[3]);
             } else {
-                w0 = e4m3x4(x.A[0], x.A[1], x.A[2], x.A[3]);
-                w1 = e4m3x4(x.B[0], x.B[1], x.B[2], x.B[3]);
+                store_row(static_cast<__nv_bfloat16 *>(p.pages[kind - kK]) + dst, le, pack_pairs<kInterleaved>(x));
             }
-            *reinterpret_cast<uint32_t *>(out + le.e0) = w0;
-            *reinterpret_cast<uint32_t *>(out + le.e1) = w1;
-        } else {
-            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.pages[kind - kK]) + dst;
-            *reinterpret_cast<uint2 *>(out + le.e0) = o0;
-            *reinterpret_cast<uint2 *>(out + le.e1) = o1;
+        }
+    };
+
+    int next = first;
+#pragma unroll
+    for (int s = 0; s < kStages; ++s, next += step)
+        issue(next, s);
+    for (int unit = first; unit < n_units;) {
+#pragma unroll
+        for (int s = 0; s < kStages; ++s) {
+            if (unit >= n_units)
+                break;
+            copy_wait<kStages - 1>();
+            consume(unit, s);
+            issue(next, s);
+            unit += step;
+            next += step;
         }
     }
+    copy_wait<0>();
 }
 
 template <bool kInterleaved, bool kFp8>
@@ -192,8 +211,11 @@ cudaError_t launch(const AppendArgs &a, cudaStream_t stream)
         p.src[i].x = static_cast<const __nv_bfloat16 *>(x[i]);
         p.src[i].w = static_cast<const __nv_bfloat16 *>(w[i]);
         p.src[i].xs = xs[i];
-        p.src[i].heads = FastDiv(static_cast<uint32_t>(heads[i] > 0 ? heads[i] : 1));
-        p.src[i].rows = a.B * a.S * heads[i];
+        const int per_token = (heads[i] + 1) / 2;
+        p.src[i].pairs_per_token = FastDiv(static_cast<uint32_t>(per_token > 0 ? per_token : 1));
+        p.src[i].heads = heads[i];
+        p.src[i].pairs = a.B * a.S * per_token;
+        p.src[i].units = (p.src[i].pairs + R::kRows - 1) / R::kRows;
     }
     p.q_out = static_cast<__nv_bfloat16 *>(a.q_out);
     p.qos = a.qos;
@@ -213,14 +235,22 @@ cudaError_t launch(const AppendArgs &a, cudaStream_t stream)
     p.pages_per_seq = a.pages_per_seq;
     p.cap = static_cast<long long>(a.pages_per_seq) * a.page_size;
     p.eps = a.eps;
-    constexpr int kIter = 4;
-    long long units = 0;
-    for (Source &sc : p.src) {
-        sc.units = static_cast<int>((static_cast<long long>(sc.rows) + R::kRows * kIter - 1) / (R::kRows * kIter));
-        units += sc.units;
+    // Per device, as for the other kernels: the attribute applies to the device current when it is set.
+    static bool attr_set[kMaxDevices] = {};
+    const int dev = current_device_index();
+    if (dev < 0)
+        return cudaErrorInvalidDevice;
+    if (!attr_set[dev]) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(append_kernel<kInterleaved, kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess)
+            return e;
+        attr_set[dev] = true;
     }
-    append_kernel<kInterleaved, kFp8, kIter>
-        <<<static_cast<unsigned>((units + kWarps - 1) / kWarps), kThreads, 0, stream>>>(p);
+    const long long units = static_cast<long long>(p.src[0].units) + p.src[1].units + p.src[2].units;
+    const long long want = (units + kWarps - 1) / kWarps, most = 2LL * a.sm_count;
+    append_kernel<kInterleaved, kFp8>
+        <<<static_cast<unsigned>(want < most ? want : most), kThreads, kSmem, stream>>>(p);
     return cudaGetLastError();
 }
 

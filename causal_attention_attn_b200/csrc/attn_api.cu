@@ -518,7 +518,7 @@ extern "C" const char *attn_status_string(int status)
         return "the decode needs more scratch than the fixed no-allocation buffer holds "
                "(too many (batch, kv head, head group) work units for attn_decode_noalloc)";
     case ATTN_ERR_ROTATION:
-        return "rot_dim must be a multiple of 8 in [0, D], with cos and sin tables of max_pos >= 1 rows unless it is 0";
+        return "rot_dim must be a multiple of 16 in [0, D], with cos and sin tables of max_pos >= 1 rows unless it is 0";
     case ATTN_ERR_EPS:
         return "eps must be finite and >= 0";
     default:

@@ -163,6 +163,7 @@ struct NormRopeArgs {
     int B, S, D, rot_dim, max_pos, interleaved;
     float eps;
     bool backward;
+    int sm_count;
     float *partials;   // backward with norm: [kNormRopeBwdBlocks][2][D], or null: no dw
     float *dwq, *dwk;  // [D], either may be null
 };
@@ -179,6 +180,7 @@ struct AppendArgs {
     const float *k_scale, *v_scale;  // e4m3 cache: [Hkv][128]; null: bf16 cache
     int B, Hq, Hkv, S, num_pages, page_size, pages_per_seq, rot_dim, max_pos, interleaved;
     float eps;
+    int sm_count;
     TensorStrides qs, ks, vs, qos;
 };
 cudaError_t launch_append(const AppendArgs &a, cudaStream_t stream);

@@ -9,12 +9,12 @@
  * Without weights there is no norm: z = R x and dx = R^T dz.
  *
  * Bound by memory: forward reads and writes each row once, backward reads two and writes one, with
- * about a dozen operations an element. So the design is about loads in flight and about instructions
- * per byte: a row lies in D / 8 lanes (head_row.cuh), each lane issues the loads of kIter rows before
- * it uses the first, and rows are numbered (token, head) so that consecutive rows of a warp mostly
- * share a token and its angles. The weight's gradient stays in registers over all rows of a warp,
- * then goes through shared memory to one partial per block; a second small kernel adds the
- * partials in a fixed order, so the result does not depend on timing (no atomics).
+ * about a dozen operations an element. So the design is about bytes in flight and instructions per
+ * byte: head_row.cuh has the layout of rows over lanes and the ring that keeps kStages units of every
+ * warp on their way. Blocks are persistent (two per SM), their warps take every (number of warps)-th
+ * unit of q, then of k. The weight's gradient stays in registers over all units of a warp, then
+ * goes through shared memory to one partial per block; a second small kernel adds the partials in a
+ * fixed order, so the result does not depend on timing (no atomics).
  */
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -30,14 +30,14 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
-// One of q and k: its rows are numbered token * H + head, token = b * S + i.
+// One of q and k. A pair is two neighbouring heads of one token (the second may be missing), numbered
+// token * ceil(H / 2) + pair, token = b * S + i; a unit is the kRows pairs that a warp takes at once.
 struct Side {
     const __nv_bfloat16 *x, *w, *dz;
     __nv_bfloat16 *out;  // z, or dx
     TensorStrides xs, zs, os;
-    FastDiv heads;
-    int rows;   // B * S * H
-    int units;  // warp-sized pieces of kRows * kIter rows
+    FastDiv pairs_per_token;
+    int heads, pairs, units;
 };
 
 struct NormRopeParams {
@@ -49,187 +49,208 @@ struct NormRopeParams {
     float *partials;  // backward: [block][2][D]
 };
 
-// A lane's place in one row.
-struct RowAt {
-    bool live;
-    int pos;            // position of the rotation
-    long long x, z, o;  // element offsets of the row
+// A lane's place: one pair of rows.
+struct PairAt {
+    bool live0, live1;  // the pair's rows exist
+    bool has;           // their position has angles (or there is no rotation)
+    uint32_t b, i, h;
+    __device__ __forceinline__ long long offset(const TensorStrides &s) const { return b * s.b + h * s.h + i * s.s; }
 };
 
-__device__ __forceinline__ RowAt locate_row(const NormRopeParams &p, const Side &sd, int row)
+__device__ __forceinline__ PairAt locate_pair(const Side &sd, const FastDiv &seq, int pair, uint32_t *tok)
 {
-    RowAt r;
-    r.live = row < sd.rows;
-    const uint32_t n = r.live ? static_cast<uint32_t>(row) : 0u;
-    const uint32_t tok = sd.heads.quot(n), h = n - tok * sd.heads.d;
-    const uint32_t b = p.seq.quot(tok), i = tok - b * p.seq.d;
-    r.pos = p.positions ? __ldg(p.positions + tok) : static_cast<int>(i);
-    r.x = b * sd.xs.b + h * sd.xs.h + i * sd.xs.s;
-    r.z = b * sd.zs.b + h * sd.zs.h + i * sd.zs.s;
-    r.o = b * sd.os.b + h * sd.os.h + i * sd.os.s;
+    PairAt r;
+    r.live0 = pair < sd.pairs;
+    const uint32_t n = r.live0 ? static_cast<uint32_t>(pair) : 0u;
+    *tok = sd.pairs_per_token.quot(n);
+    r.h = 2 * (n - *tok * sd.pairs_per_token.d);
+    r.live1 = r.live0 && static_cast<int>(r.h) + 1 < sd.heads;
+    r.b = seq.quot(*tok);
+    r.i = *tok - r.b * seq.d;
     return r;
 }
 
-// A plain load: the output may be the input (attn.h), so it is not read-only data.
-__device__ __forceinline__ uint2 load_quad(const __nv_bfloat16 *p) { return *reinterpret_cast<const uint2 *>(p); }
+template <bool kBackward>
+struct Ring {
+    // Forward: 3 stages of 4 KB a warp; backward (x and dz): 2 of 6 KB. Either way 96 KB of shared
+    // memory a block, two blocks an SM, and 96 to 128 KB of rows in flight on each SM.
+    static constexpr int kStages = kBackward ? 2 : 3;
+    static constexpr int kX = 0, kDz = 2 * kRowSlots;
+    static constexpr int kAngles = kBackward ? 4 * kRowSlots : 2 * kRowSlots;
+    static constexpr int kStageBytes = (kAngles + kAngleSlots) * kSlotBytes;
+    static constexpr int kBytes = kWarps * kStages * kStageBytes;
+};
 
-template <int D, bool kInterleaved, int kIter>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParams p)
+template <int D, bool kInterleaved, bool kBackward>
+__global__ void __launch_bounds__(kThreads, 2) norm_rope_kernel(const NormRopeParams p)
 {
     using R = RowLanes<D>;
-    const int lane = threadIdx.x & 31;
-    const int l = lane & (R::kLanes - 1);
-    const int unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const bool is_k = unit >= p.side[0].units;
-    if (is_k && unit - p.side[0].units >= p.side[1].units)
-        return;
-    const Side &sd = p.side[is_k ? 1 : 0];
-    const int row0 = (unit - (is_k ? p.side[0].units : 0)) * (R::kRows * kIter) + lane / R::kLanes;
+    using G = Ring<kBackward>;
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int l = lane & (R::kLanes - 1), group = lane / R::kLanes;
     const LaneElems le = lane_elems<kInterleaved>(l, p.table.rot);
+    const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(warp * G::kStages * G::kStageBytes + lane * 16);
+    const int n_q = p.side[0].units, n_units = n_q + p.side[1].units;
+    const int step = gridDim.x * kWarps;
+    const int first = blockIdx.x * kWarps + warp;
 
-    RowAt at[kIter];
-    uint2 g0[kIter], g1[kIter];
-    float4 c[kIter], s[kIter];
-#pragma unroll
-    for (int k = 0; k < kIter; ++k) {
-        at[k] = locate_row(p, sd, row0 + k * R::kRows);
-        g0[k] = g1[k] = make_uint2(0u, 0u);
-        if (at[k].live) {
-            g0[k] = load_quad(sd.x + at[k].x + le.e0);
-            g1[k] = load_quad(sd.x + at[k].x + le.e1);
+    // Starts the copies of one unit into stage s; an empty group behind the last unit.
+    PairAt at[G::kStages];
+    auto issue = [&](int unit, int s) {
+        if (unit < n_units) {
+            const bool is_k = unit >= n_q;
+            const Side &sd = p.side[is_k ? 1 : 0];
+            uint32_t tok;
+            PairAt a = locate_pair(sd, p.seq, (unit - (is_k ? n_q : 0)) * R::kRows + group, &tok);
+            const uint32_t base = ring + static_cast<uint32_t>(s * G::kStageBytes);
+            if (kBackward) {
+                const __nv_bfloat16 *dz = sd.dz + a.offset(sd.zs);
+                copy_row(base + G::kDz * kSlotBytes, dz, le, a.live0);
+                copy_row(base + (G::kDz + kRowSlots) * kSlotBytes, a.live1 ? dz + sd.zs.h : dz, le, a.live1);
+            }
+            if (!kBackward || sd.w) {
+                const __nv_bfloat16 *x = sd.x + a.offset(sd.xs);
+                copy_row(base + G::kX * kSlotBytes, x, le, a.live0);
+                copy_row(base + (G::kX + kRowSlots) * kSlotBytes, a.live1 ? x + sd.xs.h : x, le, a.live1);
+            }
+            const int pos = p.positions ? __ldg(p.positions + tok) : static_cast<int>(a.i);
+            a.has = p.table.has(pos);
+            if (le.rotated && a.has)
+                copy_angles(base + G::kAngles * kSlotBytes, p.table, pos, l);
+            at[s] = a;
         }
-    }
+        copy_commit();
+    };
+
+    Pairs dw;
+    float *red = reinterpret_cast<float *>(smem + G::kBytes);  // backward: [side][warp][D] sums
+    // The sums of one side: over the lanes that hold the same channels, then to the warp's row.
+    auto flush_dw = [&](int side) {
+        if constexpr (kBackward) {
+            float *mine = red + (side * kWarps + warp) * D;
 #pragma unroll
-    for (int k = 0; k < kIter; ++k)
-        load_angles(p.table, at[k].pos, l, le.rotated && at[k].live, c[k], s[k]);
-    const bool norm = sd.w != nullptr;
-    Pairs w;
-    if (norm)
-        w = load_weight<kInterleaved>(sd.w, le);
+            for (int u = 0; u < 8; ++u) {
 #pragma unroll
-    for (int k = 0; k < kIter; ++k) {
-        Pairs x = unpack_pairs<kInterleaved>(g0[k], g1[k]);
-        if (norm) {
-            const float r = rsqrtf(row_sum<D>(pairs_dot(x, x)) * (1.f / D) + p.eps);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                x.A[u] *= r * w.A[u];
-                x.B[u] *= r * w.B[u];
+                for (int o = R::kLanes; o < 32; o <<= 1) {
+                    dw.A[u] += __shfl_xor_sync(0xffffffffu, dw.A[u], o);
+                    dw.B[u] += __shfl_xor_sync(0xffffffffu, dw.B[u], o);
+                }
+                if (group == 0) {
+                    mine[elem_a<kInterleaved>(le, u)] = dw.A[u];
+                    mine[elem_b<kInterleaved>(le, u)] = dw.B[u];
+                }
+                dw.A[u] = dw.B[u] = 0.f;
             }
         }
-        if (le.rotated)
-            rotate_pairs(x, c[k], s[k]);
-        uint2 o0, o1;
-        pack_pairs<kInterleaved>(x, o0, o1);
-        // A position without a row of the tables: a row of zeros.
-        if (p.table.rot && (at[k].pos < 0 || at[k].pos >= p.table.max_pos))
-            o0 = o1 = make_uint2(0u, 0u);
-        if (at[k].live) {
-            *reinterpret_cast<uint2 *>(sd.out + at[k].o + le.e0) = o0;
-            *reinterpret_cast<uint2 *>(sd.out + at[k].o + le.e1) = o1;
-        }
+    };
+    if constexpr (kBackward) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            dw.A[u] = dw.B[u] = 0.f;
     }
-}
 
-template <int D, bool kInterleaved, int kIter>
-__global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const NormRopeParams p)
-{
-    using R = RowLanes<D>;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int l = lane & (R::kLanes - 1);
-    const LaneElems le = lane_elems<kInterleaved>(l, p.table.rot);
-    __shared__ float red[kWarps][R::kRows][D];
-#pragma unroll 1
-    for (int side = 0; side < 2; ++side) {
-        const Side &sd = p.side[side];
+    auto consume = [&](int unit, int s) {
+        const bool is_k = unit >= n_q;
+        const Side &sd = p.side[is_k ? 1 : 0];
         const bool norm = sd.w != nullptr;
-        Pairs w, dw;
+        const uint32_t base = ring + static_cast<uint32_t>(s * G::kStageBytes);
+        const PairAt a = at[s];
+        const bool turn = le.rotated && a.has;
+        __nv_bfloat16 *out = sd.out + a.offset(sd.os);
+        Angles ang;
+        if (turn)
+            ang = read_angles(base + G::kAngles * kSlotBytes);
+        const RawRow wraw = norm ? load_row(sd.w, le) : zero_row();
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-            w.A[u] = w.B[u] = dw.A[u] = dw.B[u] = 0.f;
-        if (norm)
-            w = load_weight<kInterleaved>(sd.w, le);
-        for (int unit = blockIdx.x * kWarps + warp; unit < sd.units; unit += gridDim.x * kWarps) {
-            const int row0 = unit * (R::kRows * kIter) + lane / R::kLanes;
-            RowAt at[kIter];
-            uint2 g0[kIter], g1[kIter], d0[kIter], d1[kIter];
-            float4 c[kIter], s[kIter];
-            bool in[kIter];
+        for (int k = 0; k < 2; ++k) {
+            const bool live = k ? a.live1 : a.live0;
+            // A position without a row of the tables: zeros out, and no gradient.
+            const bool in = live && a.has;
+            if constexpr (!kBackward) {
+                Pairs x = unpack_pairs<kInterleaved>(read_row(base + (G::kX + k * kRowSlots) * kSlotBytes));
+                if (norm) {
+                    const Pairs w = unpack_pairs<kInterleaved>(wraw);
+                    const float r = rsqrtf(row_sum<D>(pairs_dot(x, x)) * (1.f / D) + p.eps);
 #pragma unroll
-            for (int k = 0; k < kIter; ++k) {
-                at[k] = locate_row(p, sd, row0 + k * R::kRows);
-                // A position without a row of the tables gave zeros, so its gradient is zero.
-                in[k] = at[k].live && (!p.table.rot || (at[k].pos >= 0 && at[k].pos < p.table.max_pos));
-                g0[k] = g1[k] = d0[k] = d1[k] = make_uint2(0u, 0u);
-                if (in[k]) {
-                    d0[k] = load_quad(sd.dz + at[k].z + le.e0);
-                    d1[k] = load_quad(sd.dz + at[k].z + le.e1);
-                    if (norm) {
-                        g0[k] = load_quad(sd.x + at[k].x + le.e0);
-                        g1[k] = load_quad(sd.x + at[k].x + le.e1);
+                    for (int u = 0; u < 8; ++u) {
+                        x.A[u] *= r * w.A[u];
+                        x.B[u] *= r * w.B[u];
                     }
                 }
-            }
-#pragma unroll
-            for (int k = 0; k < kIter; ++k)
-                load_angles(p.table, at[k].pos, l, le.rotated && at[k].live, c[k], s[k]);
-#pragma unroll
-            for (int k = 0; k < kIter; ++k) {
-                Pairs dy = unpack_pairs<kInterleaved>(d0[k], d1[k]);
-                if (le.rotated)
-                    rotate_pairs(dy, c[k], make_float4(-s[k].x, -s[k].y, -s[k].z, -s[k].w));
+                if (turn)
+                    rotate_pairs<false>(x, ang);
+                if (live)
+                    store_row(out + (k ? sd.os.h : 0), le, in ? pack_pairs<kInterleaved>(x) : zero_row());
+            } else {
+                const RawRow dr = read_row(base + (G::kDz + k * kRowSlots) * kSlotBytes);
+                Pairs dy = unpack_pairs<kInterleaved>(in ? dr : zero_row());
+                if (turn)
+                    rotate_pairs<true>(dy, ang);
                 if (norm) {
-                    const Pairs x = unpack_pairs<kInterleaved>(g0[k], g1[k]);
+                    const RawRow xr = read_row(base + (G::kX + k * kRowSlots) * kSlotBytes);
+                    const Pairs w = unpack_pairs<kInterleaved>(wraw), x = unpack_pairs<kInterleaved>(in ? xr : zero_row());
                     Pairs g;
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
+                    for (int u = 0; u < 8; ++u) {
                         g.A[u] = dy.A[u] * w.A[u];
                         g.B[u] = dy.B[u] * w.B[u];
                     }
                     const float xx = row_sum<D>(pairs_dot(x, x)), gx = row_sum<D>(pairs_dot(g, x));
-                    const float r = in[k] ? rsqrtf(xx * (1.f / D) + p.eps) : 0.f;
+                    const float r = in ? rsqrtf(xx * (1.f / D) + p.eps) : 0.f;
                     const float f = r * r * (gx * (1.f / D));
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
+                    for (int u = 0; u < 8; ++u) {
                         dw.A[u] = fmaf(dy.A[u], x.A[u] * r, dw.A[u]);
                         dw.B[u] = fmaf(dy.B[u], x.B[u] * r, dw.B[u]);
                         dy.A[u] = r * fmaf(-f, x.A[u], g.A[u]);
                         dy.B[u] = r * fmaf(-f, x.B[u], g.B[u]);
                     }
                 }
-                if (at[k].live) {
-                    uint2 o0, o1;
-                    pack_pairs<kInterleaved>(dy, o0, o1);
-                    *reinterpret_cast<uint2 *>(sd.out + at[k].o + le.e0) = o0;
-                    *reinterpret_cast<uint2 *>(sd.out + at[k].o + le.e1) = o1;
-                }
+                if (live)
+                    store_row(out + (k ? sd.os.h : 0), le, pack_pairs<kInterleaved>(dy));
             }
         }
-        if (!p.partials)
-            continue;
-        // The block's partial: every lane's sums, in channel order, added in a fixed order.
-        float *mine = red[warp][lane / R::kLanes];
+    };
+
+    int next = first;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            if constexpr (kInterleaved) {
-                mine[(u < 2 ? le.e0 : le.e1) + 2 * (u & 1)] = dw.A[u];
-                mine[(u < 2 ? le.e0 : le.e1) + 2 * (u & 1) + 1] = dw.B[u];
-            } else {
-                mine[le.e0 + u] = dw.A[u];
-                mine[le.e1 + u] = dw.B[u];
+    for (int s = 0; s < G::kStages; ++s, next += step)
+        issue(next, s);
+    bool on_k = false;
+    for (int unit = first; unit < n_units;) {
+#pragma unroll
+        for (int s = 0; s < G::kStages; ++s) {
+            if (unit >= n_units)
+                break;
+            copy_wait<G::kStages - 1>();
+            if (kBackward && !on_k && unit >= n_q) {  // this warp's first unit of k
+                flush_dw(0);
+                on_k = true;
             }
+            consume(unit, s);
+            issue(next, s);
+            unit += step;
+            next += step;
         }
+    }
+    copy_wait<0>();
+    if constexpr (kBackward) {
+        flush_dw(on_k ? 1 : 0);
+        if (!p.partials)
+            return;
+        if (!on_k)
+            flush_dw(1);  // no unit of k: zeros
+        // The block's partial: the warps' sums in order.
         __syncthreads();
-        for (int d = threadIdx.x; d < D; d += kThreads) {
+        for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+            const int side = i / D, d = i % D;
             float t = 0.f;
 #pragma unroll
             for (int v = 0; v < kWarps; ++v)
-#pragma unroll
-                for (int j = 0; j < R::kRows; ++j)
-                    t += red[v][j][d];
-            p.partials[(static_cast<size_t>(blockIdx.x) * 2 + side) * D + d] = t;
+                t += red[(side * kWarps + v) * D + d];
+            p.partials[static_cast<size_t>(blockIdx.x) * 2 * D + i] = t;
         }
-        __syncthreads();
     }
 }
 
@@ -257,7 +278,7 @@ __global__ void __launch_bounds__(1024) weight_grad_kernel(const float *partials
     }
 }
 
-void fill_side(Side &sd, const NormRopeSide &a, int B, int S)
+void fill_side(Side &sd, const NormRopeSide &a, int B, int S, int rows)
 {
     sd.x = static_cast<const __nv_bfloat16 *>(a.x);
     sd.w = static_cast<const __nv_bfloat16 *>(a.w);
@@ -266,46 +287,55 @@ void fill_side(Side &sd, const NormRopeSide &a, int B, int S)
     sd.xs = a.xs;
     sd.zs = a.zs;
     sd.os = a.os;
-    sd.heads = FastDiv(static_cast<uint32_t>(a.H));
-    sd.rows = B * S * a.H;
+    const int per_token = (a.H + 1) / 2;
+    sd.pairs_per_token = FastDiv(static_cast<uint32_t>(per_token));
+    sd.heads = a.H;
+    sd.pairs = B * S * per_token;
+    sd.units = (sd.pairs + rows - 1) / rows;
 }
 
-template <int D, bool kInterleaved>
+template <int D, bool kInterleaved, bool kBackward>
 cudaError_t launch(const NormRopeArgs &a, cudaStream_t stream)
 {
     using R = RowLanes<D>;
     NormRopeParams p;
-    fill_side(p.side[0], a.q, a.B, a.S);
-    fill_side(p.side[1], a.k, a.B, a.S);
+    fill_side(p.side[0], a.q, a.B, a.S, R::kRows);
+    fill_side(p.side[1], a.k, a.B, a.S, R::kRows);
     p.table = RopeTable{a.cos, a.sin, a.rot_dim, a.max_pos};
     p.positions = a.positions;
     p.seq = FastDiv(static_cast<uint32_t>(a.S));
     p.eps = a.eps;
     p.partials = a.partials;
-    auto units = [&](int iter) {
-        const int per = R::kRows * iter;
-        long long n = 0;
-        for (Side &sd : p.side) {
-            sd.units = static_cast<int>((static_cast<long long>(sd.rows) + per - 1) / per);
-            n += sd.units;
-        }
-        return n;
-    };
-    if (!a.backward) {
-        const long long n = units(4);
-        norm_rope_kernel<D, kInterleaved, 4>
-            <<<static_cast<unsigned>((n + kWarps - 1) / kWarps), kThreads, 0, stream>>>(p);
-        return cudaGetLastError();
+    constexpr int kSmem = Ring<kBackward>::kBytes + (kBackward ? 2 * kWarps * D * 4 : 0);
+    // Per device, as for the other kernels: the attribute applies to the device current when it is set.
+    static bool attr_set[kMaxDevices] = {};
+    const int dev = current_device_index();
+    if (dev < 0)
+        return cudaErrorInvalidDevice;
+    if (!attr_set[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(norm_rope_kernel<D, kInterleaved, kBackward>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess)
+            return e;
+        attr_set[dev] = true;
     }
-    const long long n = units(2);
-    const long long want = (n + kWarps - 1) / kWarps;
-    const int blocks = static_cast<int>(want < kNormRopeBwdBlocks ? want : kNormRopeBwdBlocks);
-    norm_rope_bwd_kernel<D, kInterleaved, 2><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(p);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || !a.partials)
+    const long long want = (static_cast<long long>(p.side[0].units) + p.side[1].units + kWarps - 1) / kWarps;
+    const long long most = 2LL * a.sm_count < kNormRopeBwdBlocks ? 2LL * a.sm_count : kNormRopeBwdBlocks;
+    const int blocks = static_cast<int>(want < most ? want : most);
+    norm_rope_kernel<D, kInterleaved, kBackward><<<static_cast<unsigned>(blocks), kThreads, kSmem, stream>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !kBackward || !a.partials)
         return e;
     weight_grad_kernel<<<dim3(D / 32, 2), 1024, 0, stream>>>(a.partials, blocks, D, a.dwq, a.dwk);
     return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_d(const NormRopeArgs &a, cudaStream_t stream)
+{
+    if (a.backward)
+        return a.interleaved ? launch<D, true, true>(a, stream) : launch<D, false, true>(a, stream);
+    return a.interleaved ? launch<D, true, false>(a, stream) : launch<D, false, false>(a, stream);
 }
 
 }  // namespace
@@ -314,11 +344,11 @@ cudaError_t launch_norm_rope(const NormRopeArgs &a, cudaStream_t stream)
 {
     switch (a.D) {
     case 32:
-        return a.interleaved ? launch<32, true>(a, stream) : launch<32, false>(a, stream);
+        return launch_d<32>(a, stream);
     case 64:
-        return a.interleaved ? launch<64, true>(a, stream) : launch<64, false>(a, stream);
+        return launch_d<64>(a, stream);
     case 128:
-        return a.interleaved ? launch<128, true>(a, stream) : launch<128, false>(a, stream);
+        return launch_d<128>(a, stream);
     default:
         return cudaErrorInvalidValue;
     }

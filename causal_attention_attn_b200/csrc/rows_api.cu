@@ -33,7 +33,7 @@ int check_row_args(const void *q_weight, const void *k_weight, const float *cos,
 {
     if (interleaved != 0 && interleaved != 1)
         return ATTN_ERR_SHAPE;
-    if (rot_dim < 0 || rot_dim > D || rot_dim % 8 != 0 || (rot_dim > 0 && max_pos < 1))
+    if (rot_dim < 0 || rot_dim > D || rot_dim % 16 != 0 || (rot_dim > 0 && max_pos < 1))
         return ATTN_ERR_ROTATION;
     if (rot_dim > 0 && (!cos || !sin))
         return ATTN_ERR_NULL;
@@ -98,6 +98,7 @@ int norm_rope(const void *q, const void *k, const void *q_weight, const void *k_
     a.interleaved = interleaved;
     a.eps = eps;
     a.backward = backward;
+    a.sm_count = sms;
     a.partials = want_dw ? static_cast<float *>(workspace) : nullptr;
     a.dwq = dq_weight;
     a.dwk = dk_weight;
@@ -179,6 +180,7 @@ int append_paged(const void *q, const void *k, const void *v, const void *q_weig
     a.max_pos = max_pos;
     a.interleaved = interleaved;
     a.eps = eps;
+    a.sm_count = sms;
     if (launch_append(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
         cudaGetLastError();
         return ATTN_ERR_LAUNCH;

@@ -60,7 +60,7 @@ typedef enum attn_status {
     ATTN_ERR_SCALE = -11,           /* scale is not finite and > 0 */
     ATTN_ERR_CUDA = -12,            /* a CUDA runtime call failed (device query, tensor map, copy) */
     ATTN_ERR_SCRATCH_LIMIT = -13,   /* attn_decode_noalloc: the problem needs more scratch than its fixed buffer */
-    ATTN_ERR_ROTATION = -14,        /* rot_dim is not a multiple of 8 in [0, D], or its tables have no row */
+    ATTN_ERR_ROTATION = -14,        /* rot_dim is not a multiple of 16 in [0, D], or its tables have no row */
     ATTN_ERR_EPS = -15              /* eps is not finite and >= 0 */
 } attn_status;
 
@@ -377,7 +377,7 @@ int attn_lse_merge(float *o_acc, float *lse_acc, const void *o_part, const float
  *   positions        int32 [B, S] on the device, or NULL: row i of every batch entry is at position
  *                    i. A position outside [0, max_pos) reads no table: that token's rows of q_out
  *                    and k_out are zeros (unless rot_dim is 0, when positions are not looked at).
- *   D                32, 64 or 128. rot_dim: a multiple of 8 in [0, D].
+ *   D                32, 64 or 128. rot_dim: a multiple of 16 in [0, D].
  *   eps              finite and >= 0.
  * Hq and Hkv need not divide one another here. Pointers 16-byte aligned (positions: 4). Never
  * allocates or synchronises; returns ATTN_OK or a negative attn_status (before any launch).

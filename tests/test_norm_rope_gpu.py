@@ -53,9 +53,9 @@ CASES = [
     (3, 5, 3, 17, 64, 64, True, True, False),        # heads that do not divide, odd counts
     (3, 10, 2, 77, 64, 32, False, True, True),       # half of each head rotated
     (2, 7, 1, 19, 32, 32, False, True, False),
-    (2, 3, 2, 33, 32, 24, True, True, True),         # three lanes of four rotated
-    (1, 4, 4, 65, 128, 72, False, True, False),      # nine lanes of sixteen
-    (2, 4, 2, 21, 128, 8, False, True, False),       # four channel pairs
+    (2, 3, 2, 33, 32, 16, True, True, True),         # one lane of two rotated
+    (1, 4, 4, 65, 128, 80, False, True, False),      # five lanes of eight
+    (2, 4, 2, 21, 128, 16, False, True, False),      # one lane of eight
     (2, 6, 2, 25, 128, 128, False, False, True),     # rotation only
     (2, 6, 2, 25, 64, 0, False, True, False),        # norm only
     (1, 2, 2, 9, 32, 0, True, False, False),         # neither: a copy

@@ -47,9 +47,9 @@ def forward(lib, **kw):
     ("misaligned positions", dict(pos=A[6] + 2), -5),
     ("stride of 4", dict(ks=(4096, 4, 1024)), -5),
     ("stride of 0", dict(qs=(0, 128, 1024)), -5),
-    ("rot_dim 12", dict(rot=12), -14),
-    ("rot_dim above D", dict(rot=72), -14),
-    ("negative rot_dim", dict(rot=-8), -14),
+    ("rot_dim 24", dict(rot=24), -14),
+    ("rot_dim above D", dict(rot=80), -14),
+    ("negative rot_dim", dict(rot=-16), -14),
     ("no table rows", dict(max_pos=0), -14),
     ("negative eps", dict(eps=-1.0), -15),
     ("nan eps", dict(eps=float("nan")), -15),
