@@ -6,7 +6,9 @@
  *
  * Row arithmetic as in norm_rope_sm100.cu. With an e4m3 cache a key or value element x is stored as
  * the code nearest to x / coefficient (ties to even, saturating at +-448), from the fp32 value: a key
- * is rounded once, not to bf16 first.
+ * is rounded once, not to bf16 first. The quotient is __fdividef's (within 2 units in the last place
+ * for coefficients in [2^-126, 2^126]): only a quotient within 2^-22 of halfway between two codes can
+ * take the other one, and exact division cost 18 us of 94 for 16384 tokens.
  *
  * Bound by memory (each new row read and written once), and for a few tokens by the launch and one
  * chain of dependent loads: length, block-table entry and angles, store. The persistent blocks and
@@ -121,6 +123,9 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendParams 
         copy_commit();
     };
 
+    // The weight of the kind that the warp is at (q, then k, then v): read once for each.
+    Pairs w;
+    Kind have_w = kV;
     auto consume = [&](int unit, int s) {
         const Kind kind = kind_of(unit);
         const Source &sc = p.src[kind];
@@ -128,23 +133,21 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendParams 
         const At a = at[s];
         const bool write = a.token && a.page >= 0 && a.page < p.num_pages;
         const bool norm = sc.w != nullptr, turn = kind != kV && le.rotated && a.token;
+        if (norm && kind != have_w) {
+            w = unpack_pairs<kInterleaved>(load_row(sc.w, le));
+            have_w = kind;
+        }
         Angles ang;
         if (turn)
             ang = read_angles(base + kAngles * kSlotBytes);
-        const RawRow wraw = norm ? load_row(sc.w, le) : zero_row();
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const bool live = k ? a.live1 : a.live0;
             const uint32_t h = a.h + k;
             Pairs x = unpack_pairs<kInterleaved>(read_row(base + k * kRowSlots * kSlotBytes));
             if (norm) {
-                const Pairs w = unpack_pairs<kInterleaved>(wraw);
                 const float r = rsqrtf(row_sum<kD>(pairs_dot(x, x)) * (1.f / kD) + p.eps);
-#pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    x.A[u] *= r * w.A[u];
-                    x.B[u] *= r * w.B[u];
-                }
+                scale_pairs(x, r, w);
             }
             if (turn)
                 rotate_pairs<false>(x, ang);
@@ -159,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendParams 
             const size_t dst = ((static_cast<size_t>(a.page) * p.Hkv + h) * p.page_size.d + a.slot) * kD;
             if constexpr (kFp8) {
                 const float *cf = p.coef[kind - kK] + h * kD;
-                uint32_t w[4];
+                uint32_t codes[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {  // four elements at a time, in element order
                     const float4 f = __ldg(reinterpret_cast<const float4 *>(cf + (j < 2 ? le.e0 : le.e1) + 4 * (j & 1)));
@@ -169,11 +172,11 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendParams 
                         const int e = 4 * j + t;  // of the lane's sixteen
                         v[t] = kInterleaved ? ((e & 1) ? x.B[e >> 1] : x.A[e >> 1]) : (e < 8 ? x.A[e & 7] : x.B[e & 7]);
                     }
-                    w[j] = e4m3x4(v[0] / f.x, v[1] / f.y, v[2] / f.z, v[3] / f.w);
+                    codes[j] = e4m3x4(__fdividef(v[0], f.x), __fdividef(v[1], f.y), __fdividef(v[2], f.z), __fdividef(v[3], f.w));
                 }
                 uint8_t *out = static_cast<uint8_t *>(p.pages[kind - kK]) + dst;
-                *reinterpret_cast<uint2 *>(out + le.e0) = make_uint2(w[0], w[1]);
-                *reinterpret_cast<uint2 *>(out + le.e1) = make_uint2(w[2], w[3]);
+                *reinterpret_cast<uint2 *>(out + le.e0) = make_uint2(codes[0], codes[1]);
+                *reinterpret_cast<uint2 *>(out + le.e1) = make_uint2(codes[2], codes[3]);
             } else {
                 store_row(static_cast<__nv_bfloat16 *>(p.pages[kind - kK]) + dst, le, pack_pairs<kInterleaved>(x));
             }

@@ -247,16 +247,32 @@ __device__ __forceinline__ Angles read_angles(uint32_t src)
     return a;
 }
 
+// Two fp32 operations an instruction: the pairs' neighbours go together.
+__device__ __forceinline__ float2 two(const float *x) { return make_float2(x[0], x[1]); }
+__device__ __forceinline__ void put_two(float *x, float2 v) { x[0] = v.x, x[1] = v.y; }
+
+// x <- x r w.
+__device__ __forceinline__ void scale_pairs(Pairs &x, float r, const Pairs &w)
+{
+    const float2 rr = make_float2(r, r);
+#pragma unroll
+    for (int u = 0; u < 8; u += 2) {
+        put_two(x.A + u, __fmul2_rn(two(x.A + u), __fmul2_rn(rr, two(w.A + u))));
+        put_two(x.B + u, __fmul2_rn(two(x.B + u), __fmul2_rn(rr, two(w.B + u))));
+    }
+}
+
 // (A, B) turned by the angles; kBack: by their negatives. Only for a lane that is rotated: an element
 // behind rot has no angle, and an infinite neighbour times sin 0 would make it NaN.
 template <bool kBack>
 __device__ __forceinline__ void rotate_pairs(Pairs &x, const Angles &t)
 {
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-        const float a = x.A[u], b = x.B[u], s = kBack ? -t.s[u] : t.s[u];
-        x.A[u] = a * t.c[u] - b * s;
-        x.B[u] = b * t.c[u] + a * s;
+    for (int u = 0; u < 8; u += 2) {
+        const float2 a = two(x.A + u), b = two(x.B + u), c = two(t.c + u), s = two(t.s + u);
+        const float2 n = make_float2(-s.x, -s.y);
+        put_two(x.A + u, __ffma2_rn(a, c, __fmul2_rn(b, kBack ? s : n)));
+        put_two(x.B + u, __ffma2_rn(b, c, __fmul2_rn(a, kBack ? n : s)));
     }
 }
 

@@ -87,6 +87,8 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_kernel(const NormRopePa
     using R = RowLanes<D>;
     using G = Ring<kBackward>;
     extern __shared__ __align__(16) uint8_t smem[];
+    if (kBackward)
+        asm volatile("griddepcontrol.launch_dependents;");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int l = lane & (R::kLanes - 1), group = lane / R::kLanes;
     const LaneElems le = lane_elems<kInterleaved>(l, p.table.rot);
@@ -121,6 +123,18 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_kernel(const NormRopePa
             at[s] = a;
         }
         copy_commit();
+    };
+
+    // The weight of the side that the warp is at (units of q come first): read once for each.
+    // (Backward keeps it packed: its unpacked registers would not fit.)
+    Pairs w;
+    RawRow wraw;
+    auto load_weight = [&](int side) {
+        if (p.side[side].w) {
+            wraw = load_row(p.side[side].w, le);
+            if constexpr (!kBackward)
+                w = unpack_pairs<kInterleaved>(wraw);
+        }
     };
 
     Pairs dw;
@@ -161,7 +175,6 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_kernel(const NormRopePa
         Angles ang;
         if (turn)
             ang = read_angles(base + G::kAngles * kSlotBytes);
-        const RawRow wraw = norm ? load_row(sd.w, le) : zero_row();
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const bool live = k ? a.live1 : a.live0;
@@ -170,13 +183,8 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_kernel(const NormRopePa
             if constexpr (!kBackward) {
                 Pairs x = unpack_pairs<kInterleaved>(read_row(base + (G::kX + k * kRowSlots) * kSlotBytes));
                 if (norm) {
-                    const Pairs w = unpack_pairs<kInterleaved>(wraw);
                     const float r = rsqrtf(row_sum<D>(pairs_dot(x, x)) * (1.f / D) + p.eps);
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        x.A[u] *= r * w.A[u];
-                        x.B[u] *= r * w.B[u];
-                    }
+                    scale_pairs(x, r, w);
                 }
                 if (turn)
                     rotate_pairs<false>(x, ang);
@@ -189,13 +197,9 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_kernel(const NormRopePa
                     rotate_pairs<true>(dy, ang);
                 if (norm) {
                     const RawRow xr = read_row(base + (G::kX + k * kRowSlots) * kSlotBytes);
-                    const Pairs w = unpack_pairs<kInterleaved>(wraw), x = unpack_pairs<kInterleaved>(in ? xr : zero_row());
-                    Pairs g;
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        g.A[u] = dy.A[u] * w.A[u];
-                        g.B[u] = dy.B[u] * w.B[u];
-                    }
+                    const Pairs x = unpack_pairs<kInterleaved>(in ? xr : zero_row());
+                    Pairs g = dy;
+                    scale_pairs(g, 1.f, unpack_pairs<kInterleaved>(wraw));
                     const float xx = row_sum<D>(pairs_dot(x, x)), gx = row_sum<D>(pairs_dot(g, x));
                     const float r = in ? rsqrtf(xx * (1.f / D) + p.eps) : 0.f;
                     const float f = r * r * (gx * (1.f / D));
@@ -217,15 +221,17 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_kernel(const NormRopePa
 #pragma unroll
     for (int s = 0; s < G::kStages; ++s, next += step)
         issue(next, s);
-    bool on_k = false;
+    bool on_k = first >= n_q;
+    load_weight(on_k ? 1 : 0);
     for (int unit = first; unit < n_units;) {
 #pragma unroll
         for (int s = 0; s < G::kStages; ++s) {
             if (unit >= n_units)
                 break;
             copy_wait<G::kStages - 1>();
-            if (kBackward && !on_k && unit >= n_q) {  // this warp's first unit of k
+            if (!on_k && unit >= n_q) {  // this warp's first unit of k
                 flush_dw(0);
+                load_weight(1);
                 on_k = true;
             }
             consume(unit, s);
@@ -239,8 +245,8 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_kernel(const NormRopePa
         flush_dw(on_k ? 1 : 0);
         if (!p.partials)
             return;
-        if (!on_k)
-            flush_dw(1);  // no unit of k: zeros
+        if (!on_k || first >= n_q)
+            flush_dw(on_k ? 0 : 1);  // no unit of the other side: zeros
         // The block's partial: the warps' sums in order.
         __syncthreads();
         for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
@@ -262,6 +268,9 @@ __global__ void __launch_bounds__(1024) weight_grad_kernel(const float *partials
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int side = blockIdx.y, d = blockIdx.x * 32 + lane;
     float *dst = side ? dwk : dwq;
+    // Launched while the gradient's last blocks still run (see the launch): their partials are complete
+    // only behind this.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!dst)
         return;
     float t = 0.f;
@@ -326,8 +335,17 @@ cudaError_t launch(const NormRopeArgs &a, cudaStream_t stream)
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !kBackward || !a.partials)
         return e;
-    weight_grad_kernel<<<dim3(D / 32, 2), 1024, 0, stream>>>(a.partials, blocks, D, a.dwq, a.dwk);
-    return cudaGetLastError();
+    // Programmatic launch: the second kernel's launch overlaps the first one's end.
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(D / 32, 2);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, weight_grad_kernel, static_cast<const float *>(a.partials), blocks, D, a.dwq, a.dwk);
 }
 
 template <int D>

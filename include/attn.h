@@ -450,7 +450,9 @@ int attn_append_paged(const void *q, const void *k, const void *v, const void *q
  * attn_append_paged_fp8 — attn_append_paged to an e4m3 cache (attn_decode_paged_fp8's): the stored
  * code of a key or value element x of kv head g, channel d is the e4m3 value nearest to
  * x / k_scale[g, d] (v_scale), ties to even, magnitudes above 448 stored as 448, NaN as NaN; x is the
- * fp32 value, not rounded to bf16 first. k_scale, v_scale: fp32 [Hkv, 128], the cache's coefficients.
+ * fp32 value, not rounded to bf16 first, and the quotient is computed in fp32 to within 2 units in
+ * the last place. k_scale, v_scale: fp32 [Hkv, 128], the cache's coefficients, each in
+ * [2^-126, 2^126].
  * Every other argument and rule is attn_append_paged's.
  */
 int attn_append_paged_fp8(const void *q, const void *k, const void *v, const void *q_weight, const void *k_weight,

@@ -61,12 +61,14 @@ def check(k_pages, v_pages, pages, coef, expect):
     for n, (b, i, pg, slot) in enumerate(where):
         keep[pg, slot] = False
         if fp8:
-            # k: half a step of e4m3 (2^-4 relative, 2^-10 among its subnormals) beside the fp32 error.
-            t = (kz[n] / coef[0].double()).clamp(-448, 448)
-            fp32 = (kb[n] - ref.BF16 * kz[n].abs()).clamp(min=0) / coef[0].double() + 4 * ref.U * t.abs()
-            ref.within(e4m3(new[0][pg, :, slot]), t, torch.clamp(t.abs() / 16, min=2.0 ** -10) + 2 * fp32, f"k row {n}")
-            want = (vz[n].float() / coef[1]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
-            assert torch.equal(new[1][pg, :, slot], want), f"v row {n}"
+            # Half a step of e4m3 (2^-4 of the binade's start, 2^-10 among its subnormals), the quotient's
+            # 2 units in the last place (4 u) and, for a key, the fp32 error of x.
+            for x, err, cf, now, what in ((kz[n], kb[n] - ref.BF16 * kz[n].abs(), coef[0], new[0], "k"),
+                                          (vz[n].double(), torch.zeros_like(kz[n]), coef[1], new[1], "v")):
+                t = x / cf.double()
+                step = torch.exp2(torch.floor(torch.log2(t.abs().clamp(min=2.0 ** -6))) - 4)
+                ref.within(e4m3(now[pg, :, slot]), t.clamp(-448, 448), step + 2 * err.clamp(min=0) / cf + 4 * ref.U * t.abs(),
+                           f"{what} row {n}")
         else:
             ref.within(new[0][pg, :, slot], kz[n], kb[n], f"k row {n}")
             assert torch.equal(new[1][pg, :, slot], vz[n]), f"v row {n}"
