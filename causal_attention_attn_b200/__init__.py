@@ -12,7 +12,7 @@ def __getattr__(name):
     if name in ("attn_fwd", "attn_fwd_host", "attn_decode_paged", "attn_prefill_paged", "attn_bwd", "attn_decode_fp8",
                 "attn_prefill_fp8",
                 "attn_decode_paged_fp8", "attn_lse_merge", "attn_qk_norm_rope", "attn_qk_norm_rope_bwd",
-                "attn_append_paged", "attn_append_paged_fp8", "AttnError", "library_path", "load_library"):
+                "attn_append_paged", "attn_append_paged_fp8", "attn_decode_prefix", "decode_prefix_workspace", "AttnError", "library_path", "load_library"):
         from . import attn as _attn
 
         return getattr(_attn, name)

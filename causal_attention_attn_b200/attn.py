@@ -28,7 +28,7 @@ STATUS_NAMES = {
 EXPORTED = ("attn_fwd", "attn_fwd_ex", "attn_fwd_host", "attn_fwd_strided", "attn_decode_ctas", "attn_status_string", "attn_version",
             "attn_device_status", "attn_decode_noalloc", "attn_decode_paged", "attn_prefill_paged", "attn_bwd", "attn_decode_fp8", "attn_prefill_fp8",
             "attn_decode_paged_fp8", "attn_lse_merge", "attn_qk_norm_rope", "attn_qk_norm_rope_bwd", "attn_append_paged",
-            "attn_append_paged_fp8")
+            "attn_append_paged_fp8", "attn_decode_prefix", "attn_decode_prefix_workspace")
 
 _lock = threading.Lock()
 _lib = None
@@ -91,6 +91,10 @@ def load_library(path: str | None = None):
         lib.attn_append_paged.argtypes = [vp] * 14 + [i] * 4 + [ll3] * 4 + [i] * 6 + [f, vp]
         lib.attn_append_paged_fp8.restype = i
         lib.attn_append_paged_fp8.argtypes = [vp] * 16 + [i] * 4 + [ll3] * 4 + [i] * 6 + [f, vp]
+        lib.attn_decode_prefix.restype = i
+        lib.attn_decode_prefix.argtypes = [vp] * 10 + [ctypes.c_longlong] + [i] * 9 + [f, vp]
+        lib.attn_decode_prefix_workspace.restype = ctypes.c_longlong
+        lib.attn_decode_prefix_workspace.argtypes = [i] * 5
         if path is None:
             _lib = lib
         return lib
@@ -759,6 +763,73 @@ def attn_append_paged_fp8(k: torch.Tensor, v: torch.Tensor, cos: torch.Tensor | 
         raise TypeError("k_scale and v_scale must be torch.Tensors")
     return _append(k, v, cos, sin, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, q, q_out, q_weight,
                    k_weight, positions, new_lens, interleaved, eps, stream)
+
+
+def decode_prefix_workspace(B: int, Hq: int, Hkv: int, max_prefix_len: int, max_seq_len: int,
+                            device="cuda") -> torch.Tensor:
+    """A workspace for ``attn_decode_prefix`` calls of these sizes (or smaller ones), to be kept for as
+    long as calls, or graphs that captured them, use it. Calls that overlap need one each."""
+    device = torch.device(device)
+    with torch.cuda.device(device):
+        n = load_library().attn_decode_prefix_workspace(B, Hq, Hkv, max_prefix_len, max_seq_len)
+        if n < 0:
+            _check(int(n))
+        return torch.empty((n,), dtype=torch.uint8, device=device)
+
+
+def attn_decode_prefix(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, prefix_table: torch.Tensor,
+                       prefix_len: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                       max_prefix_len: int, max_seq_len: int, scale: float | None = None,
+                       out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                       workspace: torch.Tensor | None = None, stream=None):
+    """Single-token decode of a batch that shares a prefix through ``attn_decode_prefix``: every sequence
+    attends to the prefix's keys (read once for the batch) and to its own.
+
+    q [B, Hq, 1, 128] bf16; k_pages, v_pages [num_pages, Hkv, page_size, 128] bf16; prefix_table int32
+    [prefix_pages] and prefix_len int32 [1]; block_table int32 [B, pages_per_seq] and seq_lens int32 [B]:
+    the keys behind the prefix (all on the GPU); max_prefix_len, max_seq_len: host-side bounds of the
+    lengths. ``workspace`` from ``decode_prefix_workspace`` keeps a loop of calls from allocating.
+    Returns (o [B, Hq, 1, 128], lse [B, Hq, 1])."""
+    _check_tensor("q", q, torch.bfloat16, 4)
+    _check_tensor("k_pages", k_pages, torch.bfloat16, 4)
+    _check_tensor("v_pages", v_pages, torch.bfloat16, 4)
+    _check_tensor("prefix_table", prefix_table, torch.int32, 1)
+    _check_tensor("prefix_len", prefix_len, torch.int32, 1)
+    _check_tensor("block_table", block_table, torch.int32, 2)
+    _check_tensor("seq_lens", seq_lens, torch.int32, 1)
+    B, Hq, Sq, D = qshape = q.shape
+    num_pages, Hkv, page_size, Dk = pages = k_pages.shape
+    if Sq != 1 or v_pages.shape != pages or Dk != D or D != 128:
+        raise ValueError(f"expected q [B,Hq,1,128] and k, v pages [P,Hkv,page,128]; got {tuple(q.shape)}, "
+                         f"{tuple(k_pages.shape)}, {tuple(v_pages.shape)}")
+    rows, per_seq = block_table.shape
+    if rows != B or seq_lens.shape[0] != B or prefix_len.shape[0] != 1:
+        raise ValueError("block_table and seq_lens need one row / entry per batch element, prefix_len one entry")
+    if scale is None:
+        scale = D ** -0.5
+    out = torch.empty(qshape, dtype=torch.bfloat16, device=q.device) if out is None else out
+    lse = torch.empty((B, Hq, 1), dtype=torch.float32, device=q.device) if lse is None else lse
+    _check_tensor("out", out, torch.bfloat16, 4)
+    _check_tensor("lse", lse, torch.float32, 3)
+    if out.shape != qshape or lse.shape != (B, Hq, 1):
+        raise ValueError(f"out must be {tuple(qshape)} and lse {(B, Hq, 1)}")
+    dev = q.get_device()
+    if workspace is None:
+        workspace = decode_prefix_workspace(B, Hq, Hkv, int(max_prefix_len), int(max_seq_len), q.device)
+        if stream is not None:
+            workspace.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+    else:
+        _check_tensor("workspace", workspace, torch.uint8, 1)
+    _same_device(dev, k_pages=k_pages, v_pages=v_pages, prefix_table=prefix_table, prefix_len=prefix_len,
+                 block_table=block_table, seq_lens=seq_lens, out=out, lse=lse, workspace=workspace)
+    with _Launch(dev, stream) as handle:
+        rc = load_library().attn_decode_prefix(
+            q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), prefix_table.data_ptr(), prefix_len.data_ptr(),
+            block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+            workspace.shape[0], B, Hq, Hkv, num_pages, page_size, int(prefix_table.shape[0]), max_prefix_len, per_seq,
+            max_seq_len, scale, handle)
+    _check(rc)
+    return out, lse
 
 
 def decode_ctas(B: int, Hq: int, Hkv: int, Skv: int, D: int) -> int:

@@ -31,11 +31,16 @@ struct DeviceState {
     size_t partial_floats = 0;
     void *bwd_block = nullptr;  // backward pass: dq accumulator and per-row vectors
     size_t bwd_bytes = 0;
+    int *prefix_status = nullptr;  // attn_decode_prefix: this device's copy of g_prefix_status
     // attn_fwd_host: a stream for the copies in, one for the copies out, and the events that order
     // them against the caller's stream (created on first use, kept for the process).
     cudaStream_t copy_in = nullptr, copy_out = nullptr;
     cudaEvent_t ev_start = nullptr, ev_in = nullptr, ev_done = nullptr, ev_out = nullptr;
 };
+
+// The status word of attn_decode_prefix. It has an address of its own, not the workspace's, because a
+// captured call may be replayed after the workspace has grown and moved.
+static __device__ int g_prefix_status;
 
 std::mutex g_mutex;
 DeviceState g_dev[kMaxDevices];
@@ -536,9 +541,10 @@ extern "C" int attn_device_status(void *stream_ptr)
     DeviceState *s = device_state(&err);
     if (!s)
         return err;
-    // Two status words: the workspace's (every entry point but attn_decode_noalloc) and the one at
-    // the start of attn_decode_noalloc's fixed array (once that entry point has run on this device).
-    int *words[2] = {s->block ? s->status : nullptr, noalloc_status_word()};
+    // Three status words: the workspace's (every entry point but the two that follow), the one at the
+    // start of attn_decode_noalloc's fixed array and attn_decode_prefix's own (each once that entry
+    // point has run on this device).
+    int *words[3] = {s->block ? s->status : nullptr, noalloc_status_word(), s->prefix_status};
     bool timed_out = false;
     for (int *word : words) {
         if (!word)
@@ -726,6 +732,203 @@ extern "C" int attn_decode_paged_fp8(const void *q, const void *k_pages, const v
 {
     return decode_paged_impl(q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, o, lse, B, Hq, Hkv,
                              num_pages, page_size, pages_per_seq, max_seq_len, scale, decode_ctas, stream_ptr, true);
+}
+
+namespace {
+
+// attn_decode_prefix's workspace, cut up.
+struct PrefixSpace {
+    size_t counters, suffix_ws, o_suffix, lse_suffix, part_o, part_lse, bytes;  // byte offsets
+};
+
+PrefixSpace prefix_space(int B, int Hq, const PrefixPlan &pl, const DecodePlan &suffix)
+{
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        const size_t here = at;
+        at += (n + 255) / 256 * 256;
+        return here;
+    };
+    PrefixSpace sp;
+    const size_t rows = static_cast<size_t>(B) * Hq;
+    sp.counters = take(static_cast<size_t>(suffix.pairs) * sizeof(int));
+    sp.suffix_ws = take(suffix.partial_floats * sizeof(float));
+    sp.o_suffix = take(rows * 128 * sizeof(float));
+    sp.lse_suffix = take(rows * sizeof(float));
+    sp.part_o = take(static_cast<size_t>(pl.slots) * 256 * 128 * sizeof(float));
+    sp.part_lse = take(static_cast<size_t>(pl.slots) * 256 * sizeof(float));
+    sp.bytes = at;
+    return sp;
+}
+
+int check_prefix_sizes(int B, int Hq, int Hkv, int max_prefix_len, int max_seq_len)
+{
+    if (B < 1 || B > kPagedMaxBatch || Hq < 1 || Hkv < 1 || max_prefix_len < 0 || max_seq_len < 0)
+        return ATTN_ERR_SHAPE;
+    if (Hq % Hkv != 0)
+        return ATTN_ERR_GQA;
+    // A kv head's tiles hold at least one row of each sequence: slots * 256 rows stay below 2^31.
+    if (static_cast<long long>(B) * Hq > (1LL << 22))
+        return ATTN_ERR_SHAPE;
+    return ATTN_OK;
+}
+
+// Both plans and the workspace's parts on the current device (g_mutex held).
+int plan_prefix(const DeviceState &s, int B, int Hq, int Hkv, int max_prefix_len, int max_seq_len, PrefixPlan *pl,
+                DecodePlan *suffix, PrefixSpace *sp)
+{
+    *pl = prefix_plan(B, Hq, Hkv, max_prefix_len, s.sm_count);
+    if (decode_plan_paged(B, Hq, Hkv, max_seq_len, 0, s.sm_count, suffix) != cudaSuccess) {
+        cudaGetLastError();
+        return ATTN_ERR_SHAPE;
+    }
+    if (pl->slots * 256 > INT_MAX)
+        return ATTN_ERR_SHAPE;
+    *sp = prefix_space(B, Hq, *pl, *suffix);
+    return ATTN_OK;
+}
+
+}  // namespace
+
+extern "C" long long attn_decode_prefix_workspace(int B, int Hq, int Hkv, int max_prefix_len, int max_seq_len)
+{
+    int rc = check_prefix_sizes(B, Hq, Hkv, max_prefix_len, max_seq_len);
+    if (rc != ATTN_OK)
+        return rc;
+    std::lock_guard<std::mutex> lock(g_mutex);
+    int err = ATTN_OK;
+    DeviceState *s = device_state(&err);
+    if (!s)
+        return err;
+    PrefixPlan pl;
+    DecodePlan suffix;
+    PrefixSpace sp;
+    rc = plan_prefix(*s, B, Hq, Hkv, max_prefix_len, max_seq_len, &pl, &suffix, &sp);
+    return rc != ATTN_OK ? rc : static_cast<long long>(sp.bytes);
+}
+
+extern "C" int attn_decode_prefix(const void *q, const void *k_pages, const void *v_pages, const int *prefix_table,
+                                  const int *prefix_len, const int *block_table, const int *seq_lens, void *o,
+                                  float *lse, void *workspace, long long workspace_bytes, int B, int Hq, int Hkv,
+                                  int num_pages, int page_size, int prefix_pages, int max_prefix_len,
+                                  int pages_per_seq, int max_seq_len, float scale, void *stream_ptr)
+{
+    if (!q || !k_pages || !v_pages || !prefix_table || !prefix_len || !block_table || !seq_lens || !o || !lse || !workspace)
+        return ATTN_ERR_NULL;
+    int rc = check_prefix_sizes(B, Hq, Hkv, max_prefix_len, max_seq_len);
+    if (rc != ATTN_OK)
+        return rc;
+    const bool page_ok = page_size == 16 || page_size == 32 || page_size == 64 ||
+                         (page_size >= 128 && page_size % 128 == 0);
+    if (!page_ok || num_pages < 1 || prefix_pages < 1 || pages_per_seq < 1)
+        return ATTN_ERR_SHAPE;
+    if (static_cast<long long>(num_pages) * Hkv > INT_MAX || static_cast<long long>(B) * pages_per_seq > INT_MAX ||
+        static_cast<long long>(pages_per_seq) * page_size > INT_MAX ||
+        static_cast<long long>(prefix_pages) * page_size > INT_MAX)
+        return ATTN_ERR_SHAPE;
+    auto aligned4 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; };
+    if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o) || !aligned16(lse) ||
+        (reinterpret_cast<uintptr_t>(workspace) & 255u) || !aligned4(prefix_table) || !aligned4(prefix_len) ||
+        !aligned4(block_table) || !aligned4(seq_lens))
+        return ATTN_ERR_ALIGN;
+    if (!(scale > 0.f) || !std::isfinite(scale))
+        return ATTN_ERR_SCALE;
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+    std::lock_guard<std::mutex> lock(g_mutex);
+    int err = ATTN_OK;
+    DeviceState *s = device_state(&err);
+    if (!s)
+        return err;
+    PrefixPlan pl;
+    DecodePlan suffix;
+    PrefixSpace sp;
+    rc = plan_prefix(*s, B, Hq, Hkv, max_prefix_len, max_seq_len, &pl, &suffix, &sp);
+    if (rc != ATTN_OK)
+        return rc;
+    if (workspace_bytes < static_cast<long long>(sp.bytes))
+        return ATTN_ERR_WORKSPACE;
+    if (!s->prefix_status) {
+        void *word = nullptr;
+        if (cudaGetSymbolAddress(&word, g_prefix_status) != cudaSuccess || !word) {
+            cudaGetLastError();
+            return ATTN_ERR_CUDA;
+        }
+        s->prefix_status = static_cast<int *>(word);
+    }
+    auto at = [&](size_t off) { return static_cast<char *>(workspace) + off; };
+    PrefixArgs pa;
+    pa.q = q;
+    pa.k_pages = k_pages;
+    pa.v_pages = v_pages;
+    pa.prefix_table = prefix_table;
+    pa.prefix_len = prefix_len;
+    pa.B = B;
+    pa.Hq = Hq;
+    pa.Hkv = Hkv;
+    pa.num_pages = num_pages;
+    pa.page_size = page_size;
+    pa.prefix_pages = prefix_pages;
+    pa.max_prefix_len = max_prefix_len;
+    pa.scale = scale;
+    pa.plan = pl;
+    pa.part_o = reinterpret_cast<float *>(at(sp.part_o));
+    pa.part_lse = reinterpret_cast<float *>(at(sp.part_lse));
+    pa.counters = reinterpret_cast<int *>(at(sp.counters));
+    pa.n_counters = static_cast<int>(suffix.pairs);
+    pa.status = s->prefix_status;
+    int encode_error = 0;
+    if (launch_prefix(pa, stream, &encode_error) != cudaSuccess) {
+        cudaGetLastError();
+        return encode_error ? ATTN_ERR_CUDA : ATTN_ERR_LAUNCH;
+    }
+    const bool own = max_seq_len > 0;
+    if (own) {
+        DecodeArgs a;
+        a.q = q;
+        a.k = k_pages;
+        a.v = v_pages;
+        a.o = nullptr;
+        a.o_part = reinterpret_cast<float *>(at(sp.o_suffix));
+        a.lse = reinterpret_cast<float *>(at(sp.lse_suffix));
+        a.B = B;
+        a.Hq = Hq;
+        a.Hkv = Hkv;
+        a.Skv = 0;
+        a.D = 128;
+        a.scale = scale;
+        a.plan = suffix;
+        a.ws = reinterpret_cast<float *>(at(sp.suffix_ws));
+        a.counters = pa.counters;
+        a.status = s->prefix_status;
+        a.seq_lens = seq_lens;
+        a.block_table = block_table;
+        a.num_pages = num_pages;
+        a.page_size = page_size;
+        a.pages_per_seq = pages_per_seq;
+        a.max_seq_len = max_seq_len;
+        if (launch_decode_tc(a, stream) != cudaSuccess) {
+            cudaGetLastError();
+            return ATTN_ERR_LAUNCH;
+        }
+    }
+    PrefixMergeArgs m;
+    m.plan = pl;
+    m.B = B;
+    m.Hq = Hq;
+    const long long cap = static_cast<long long>(prefix_pages) * page_size;
+    m.cap = static_cast<int>(cap < max_prefix_len ? cap : max_prefix_len);
+    m.prefix_len = prefix_len;
+    m.part_o = pa.part_o;
+    m.part_lse = pa.part_lse;
+    m.o_suffix = own ? reinterpret_cast<float *>(at(sp.o_suffix)) : nullptr;
+    m.lse_suffix = own ? reinterpret_cast<float *>(at(sp.lse_suffix)) : nullptr;
+    m.o = o;
+    m.lse = lse;
+    if (launch_prefix_merge(m, stream) != cudaSuccess) {
+        cudaGetLastError();
+        return ATTN_ERR_LAUNCH;
+    }
+    return ATTN_OK;
 }
 
 extern "C" int attn_prefill_fp8(const void *q, const void *k8, const void *v8, const float *k_scale,

@@ -159,6 +159,9 @@ struct TcParams {
     // e4m3 cache: the bf16 queries, read by the producer, and the per-(kv head, channel) coefficients
     const __nv_bfloat16 *q;
     const float *k_scale, *v_scale;
+    // kPart: the result stays in fp32 for a merge with attention over other keys; o is then unused
+    // and lse receives log2 units.
+    float *o_part;
 };
 
 __device__ __forceinline__ float ex2(float x)
@@ -242,7 +245,7 @@ struct UnitPos {
     int local, cpp;
 };
 
-template <int G, bool kPaged, bool kFp8>
+template <int G, bool kPaged, bool kFp8, bool kPart>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const TcParams p)
@@ -696,7 +699,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (batch_len[b] != 0)
                     continue;
                 for (int h = 0; h < p.Hq; ++h) {
-                    p.o[b * p.o_sb + h * p.o_sh + i] = __float2bfloat16_rn(0.f);
+                    if constexpr (kPart)
+                        p.o_part[(static_cast<size_t>(b) * p.Hq + h) * kD + i] = 0.f;
+                    else
+                        p.o[b * p.o_sb + h * p.o_sh + i] = __float2bfloat16_rn(0.f);
                     if (i == 0)
                         p.lse[static_cast<size_t>(b) * p.Hq + h] = -INFINITY;
                 }
@@ -976,9 +982,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float o = __uint_as_float(ov[h]) / LPV * v_coef;
                 const size_t bh = static_cast<size_t>(b) * p.Hq + h0 + h;
                 if (whole_pair) {
-                    p.o[b * p.o_sb + (h0 + h) * p.o_sh + i] = __float2bfloat16_rn(o);
+                    if constexpr (kPart)
+                        p.o_part[bh * kD + i] = o;
+                    else
+                        p.o[b * p.o_sb + (h0 + h) * p.o_sh + i] = __float2bfloat16_rn(o);
                     if (i == h)
-                        p.lse[bh] = (m[h] + log2f(L)) * kLn2;
+                        p.lse[bh] = (m[h] + log2f(L)) * (kPart ? 1.f : kLn2);
                 } else {
                     slot_base[h * kD + i] = o;
                     if (i == h)
@@ -1060,9 +1069,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         O = fmaf(w, __ldcg(sb + idx), O);
                     }
                     const size_t bh = static_cast<size_t>(b) * p.Hq + h0 + h;
-                    p.o[b * p.o_sb + (h0 + h) * p.o_sh + d] = __float2bfloat16_rn(O / W);
+                    if constexpr (kPart)
+                        p.o_part[bh * kD + d] = O / W;
+                    else
+                        p.o[b * p.o_sb + (h0 + h) * p.o_sh + d] = __float2bfloat16_rn(O / W);
                     if (d == 0)
-                        p.lse[bh] = (M + log2f(W)) * kLn2;
+                        p.lse[bh] = (M + log2f(W)) * (kPart ? 1.f : kLn2);
                 }
                 if (i == 0)
                     atomicExch(&p.counters[pr], 0);  // ready for the next call
@@ -1079,7 +1091,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #undef BAR
 }
 
-template <int G, bool kPaged, bool kFp8>
+template <int G, bool kPaged, bool kFp8, bool kPart = false>
 cudaError_t prepare_g(int *ctas_per_sm)
 {
     static int cached_per_dev[kMaxDevices] = {};  // per device: attributes apply to the current one
@@ -1089,11 +1101,11 @@ cudaError_t prepare_g(int *ctas_per_sm)
         return cudaErrorInvalidDevice;
     int &cached = cached_per_dev[dev];
     if (cached == 0) {
-        cudaError_t e = cudaFuncSetAttribute(decode_tc_kernel<G, kPaged, kFp8>,
+        cudaError_t e = cudaFuncSetAttribute(decode_tc_kernel<G, kPaged, kFp8, kPart>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         int n = 0;
         if (e == cudaSuccess)
-            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_tc_kernel<G, kPaged, kFp8>, kThreads, kSmem);
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_tc_kernel<G, kPaged, kFp8, kPart>, kThreads, kSmem);
         if (e != cudaSuccess)
             return e;
         cached = n > 0 ? n : 1;
@@ -1103,10 +1115,10 @@ cudaError_t prepare_g(int *ctas_per_sm)
     return cudaSuccess;
 }
 
-template <int G, bool kPaged, bool kFp8>
+template <int G, bool kPaged, bool kFp8, bool kPart = false>
 cudaError_t launch_g(const DecodeArgs &a, cudaStream_t stream)
 {
-    cudaError_t e = prepare_g<G, kPaged, kFp8>(nullptr);
+    cudaError_t e = prepare_g<G, kPaged, kFp8, kPart>(nullptr);
     if (e != cudaSuccess)
         return e;
     auto encode = get_encode_fn();
@@ -1171,7 +1183,8 @@ cudaError_t launch_g(const DecodeArgs &a, cudaStream_t stream)
     p.q = static_cast<const __nv_bfloat16 *>(a.q);
     p.k_scale = a.k_scale;
     p.v_scale = a.v_scale;
-    decode_tc_kernel<G, kPaged, kFp8>
+    p.o_part = a.o_part;
+    decode_tc_kernel<G, kPaged, kFp8, kPart>
         <<<static_cast<unsigned>(pl.ctas), kThreads, Lay<kFp8>::kSmem, stream>>>(tq, tk, tv, p);
     return cudaGetLastError();
 }
@@ -1181,6 +1194,8 @@ cudaError_t dispatch_g(const DecodeArgs *a, cudaStream_t stream, int *ctas_per_s
 {
     if (!a)
         return fp8 ? prepare_g<G, false, true>(ctas_per_sm) : prepare_g<G, false, false>(ctas_per_sm);
+    if (a->o_part)  // the suffixes of a shared-prefix decode: paged, bf16
+        return launch_g<G, true, false, true>(*a, stream);
     if (a->fp8)
         return a->seq_lens ? launch_g<G, true, true>(*a, stream) : launch_g<G, false, true>(*a, stream);
     return a->seq_lens ? launch_g<G, true, false>(*a, stream) : launch_g<G, false, false>(*a, stream);

@@ -104,6 +104,9 @@ struct DecodeArgs {
     // [Hkv][D] coefficients (value = code * coefficient of its kv head and channel).
     bool fp8 = false;
     const float *k_scale = nullptr, *v_scale = nullptr;
+    // Paged bf16 cache of the tensor-core decode only: when given, O goes here in fp32 [B][Hq][D] (o is
+    // not written) and lse in log2 units, for a merge with attention over other keys.
+    float *o_part = nullptr;
 };
 
 // ATTN_OK with the current device's SM count, or the attn_status that says why it cannot be used.
@@ -125,6 +128,43 @@ struct PrefillFp8Args {
     int *status;  // device status word
 };
 cudaError_t launch_prefill_fp8(const PrefillFp8Args &a, cudaStream_t stream, int *encode_error);
+
+// The shared-prefix part of a decode over paged caches (head dim 128): B sequences, one new token each,
+// over the prefix's keys. The packed rows of one kv head make tiles of 128, two tiles share a list of KV
+// tiles, and the lists are cut evenly over `ctas` CTAs; every (list, CTA) segment leaves fp32 partials
+// in slot list + CTA: part_o [slots][2][128][128] normalised, part_lse [slots][2][128] in log2 units.
+struct PrefixPlan {
+    int group, sub_groups;  // query heads of a row tile's group; parts of a group above 128 heads
+    int tile_seqs;          // sequences in a tile
+    int tile_pairs;         // per head
+    long long lists, slots;
+    int ctas;
+};
+PrefixPlan prefix_plan(int B, int Hq, int Hkv, int max_prefix_len, int sm_count);
+struct PrefixArgs {
+    const void *q, *k_pages, *v_pages;
+    const int *prefix_table, *prefix_len;  // [prefix_pages], [1]
+    int B, Hq, Hkv, num_pages, page_size, prefix_pages, max_prefix_len;
+    float scale;
+    PrefixPlan plan;
+    float *part_o, *part_lse;
+    int *counters;  // n_counters ints, set to 0
+    int n_counters;
+    int *status;
+};
+cudaError_t launch_prefix(const PrefixArgs &a, cudaStream_t stream, int *encode_error);
+
+// Joins the segments' partials and the suffixes' result (o_suffix fp32 [B][Hq][128], lse_suffix log2
+// units; null: no suffixes) into o (bf16) and lse (natural log).
+struct PrefixMergeArgs {
+    PrefixPlan plan;
+    int B, Hq, cap;
+    const int *prefix_len;
+    const float *part_o, *part_lse, *o_suffix, *lse_suffix;
+    void *o;
+    float *lse;
+};
+cudaError_t launch_prefix_merge(const PrefixMergeArgs &a, cudaStream_t stream);
 
 // Backward pass (head dim 128): dq, dk, dv from q, k, v, o, dout and the forward's lse.
 struct BwdArgs {

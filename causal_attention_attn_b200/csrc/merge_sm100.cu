@@ -19,6 +19,7 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <cstdint>
 
 #include "kernels.h"
 
@@ -92,6 +93,96 @@ cudaError_t launch_lse_merge(float *o_acc, float *lse_acc, const void *o_part, c
     default:
         return cudaErrorInvalidValue;
     }
+    return cudaGetLastError();
+}
+
+namespace {
+
+// Attention of one row of a shared-prefix decode from its parts: the segments of its list of prefix
+// tiles (prefill_sm100.cu, decode_segment) and its own suffix, all fp32 with LSEs in log2 units:
+//   M = max LSE_s,  O = sum 2^(LSE_s - M) O_s / W,  lse = (M + log2 W) ln 2,  W = sum 2^(LSE_s - M).
+// One warp per row; the lanes look up the LSEs of 32 parts at a time, then each lane adds its four
+// channels over the parts. Bound by reading the parts, which the kernels before left in L2; every part
+// is read once. A row with no part (no prefix, no suffix) gives O = 0 and lse = -inf.
+__global__ void __launch_bounds__(256) prefix_merge_kernel(const PrefixMergeArgs a)
+{
+    constexpr int kTile = 128, D = 128;
+    const int lane = threadIdx.x & 31;
+    const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (row >= static_cast<long long>(a.B) * a.Hq)
+        return;
+    const int b = static_cast<int>(row / a.Hq), h = static_cast<int>(row % a.Hq);
+    const int tile = b / a.plan.tile_seqs;
+    const int in_tile = (b - tile * a.plan.tile_seqs) * a.plan.group + h % a.plan.group;
+    const long long list = static_cast<long long>(h / a.plan.group) * a.plan.tile_pairs + tile / 2;
+    const int len = min(max(__ldg(a.prefix_len), 0), a.cap);
+    const int tiles = (len + kTile - 1) / kTile;
+    const long long total = a.plan.lists * tiles;
+    const int ctas = a.plan.ctas;
+    // The CTAs from the one that holds the list's first unit to the one that holds its last; with fewer
+    // units than CTAs those between may hold none.
+    int c0 = 0, n = 0;
+    if (tiles > 0) {
+        c0 = static_cast<int>(((list * tiles + 1) * ctas - 1) / total);
+        n = static_cast<int>((((list + 1) * tiles) * ctas - 1) / total) - c0 + 1;
+    }
+    auto part_row = [&](int c) { return ((list + c) * 2 + (tile & 1)) * kTile + in_tile; };
+    auto lse_of = [&](int k) {
+        const int c = c0 + k;
+        if (k >= n || total * c / ctas >= total * (c + 1) / ctas)
+            return -INFINITY;
+        return __ldg(a.part_lse + part_row(c));
+    };
+    const float suffix = a.o_suffix ? __ldg(a.lse_suffix + row) : -INFINITY;
+    float M = suffix;
+    for (int k = 0; k < n; k += 32)
+        M = fmaxf(M, lse_of(k + lane));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float W = 0.f;
+    // A NaN LSE (from NaN scores) must not look like an empty part: M drops NaN, so weigh by the part.
+    auto weight = [&](float l) { return l == -INFINITY ? 0.f : exp2f(l - M); };
+    if (suffix != -INFINITY) {
+        const float w = weight(suffix);
+        const float4 v = __ldg(reinterpret_cast<const float4 *>(a.o_suffix + row * D) + lane);
+        acc = make_float4(w * v.x, w * v.y, w * v.z, w * v.w);
+        W = w;
+    }
+    for (int k = 0; k < n; k += 32) {
+        const float l = lse_of(k + lane);
+        const unsigned some = __ballot_sync(0xffffffffu, l != -INFINITY);
+        const float w = weight(l);
+#pragma unroll 4
+        for (int t = 0; t < min(32, n - k); ++t) {
+            const float wt = __shfl_sync(0xffffffffu, w, t);
+            if (!((some >> t) & 1u))
+                continue;
+            const float4 v = __ldg(reinterpret_cast<const float4 *>(a.part_o + part_row(c0 + k + t) * D) + lane);
+            acc.x = fmaf(wt, v.x, acc.x);
+            acc.y = fmaf(wt, v.y, acc.y);
+            acc.z = fmaf(wt, v.z, acc.z);
+            acc.w = fmaf(wt, v.w, acc.w);
+            W += wt;
+        }
+    }
+    const float inv = W == 0.f ? 0.f : 1.f / W;  // 0 only for a row without parts
+    __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+    uint2 out;
+    out.x = *reinterpret_cast<uint32_t *>(&lo);
+    out.y = *reinterpret_cast<uint32_t *>(&hi);
+    reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.o) + row * D)[lane] = out;
+    if (lane == 0)
+        a.lse[row] = W == 0.f ? -INFINITY : (M + log2f(W)) * 0.6931471805599453f;
+}
+
+}  // namespace
+
+cudaError_t launch_prefix_merge(const PrefixMergeArgs &a, cudaStream_t stream)
+{
+    const long long rows = static_cast<long long>(a.B) * a.Hq;
+    prefix_merge_kernel<<<static_cast<unsigned>((rows + 7) / 8), 256, 0, stream>>>(a);
     return cudaGetLastError();
 }
 

@@ -140,7 +140,21 @@ struct Params {
     // Paged: 1 when the (batch, query-tile) pairs are few enough (<= kMaxSorted) to be put in order of
     // their KV-tile count at the start of the kernel (the lengths are known on the device only).
     int sorted = 0;
+    // Shared prefix of a decode: one new token per sequence, rows = (sequence, query head of the kv
+    // head's group) packed into tiles of tile_seqs sequences. block_table is the prefix's one row,
+    // seq_lens its one length; O and LSE leave as fp32 partials, 256 rows for each segment.
+    int heads = 0;      // kv heads times sub_groups
+    int sub_groups = 1; // equal parts of a kv head's group of more than 128 query heads; group is one part
+    int tile_seqs = 0;  // sequences in a 128-row tile
+    int tile_pairs = 0; // pairs of tiles per head: heads * tile_pairs lists of KV tiles
+    float *part_lse = nullptr;  // [segment slot][256], log2 units
+    int *counters = nullptr;    // the suffix kernel's arrival counters, cleared here
+    int n_counters = 0;
 };
+
+// What an instantiation of the kernel computes: attention over a dense cache, over a paged,
+// variable-length one, or the shared-prefix part of a decode (see decode_segment).
+enum Mode : int { kDense = 0, kPagedCache = 1, kPrefix = 2 };
 
 // The sorted order of (batch, query-tile) pairs (e = b + B * item) and their KV-tile counts.
 constexpr int kMaxSorted = 64;
@@ -226,23 +240,79 @@ __device__ __forceinline__ int work_index(const Params &p, int r)
     return w < p.n_work ? static_cast<int>(w) : -1;
 }
 
-// One work item: two 128-row query tiles X = 0 (A), 1 (B) that stream the same K/V tiles.
+// One work item: two 128-row query tiles X = 0 (A), 1 (B) that stream the same K/V tiles. Shared
+// prefix: a segment; q0 are the tiles' first sequences, kt0 the first KV tile, slot where its partials
+// go.
 struct Item {
     int q0[2];     // first query row of each tile
     int hq[2];     // query head of each tile
     int b, kvh;    // batch entry and kv head
     int skv, off;  // keys of the sequence, and the causal offset skv - Sq
     int n[2];      // KV tiles each tile needs (0: the tile lies past Sq or sees no key)
+    int kt0, slot;
     __device__ __forceinline__ int n_max() const { return max(n[0], n[1]); }
 };
+
+// ---- shared prefix of a decode ------------------------------------------------------------------
+// For each head and pair of tiles there is a list of all KV tiles of the prefix; the lists, laid end
+// to end, are cut into one range per CTA of equal length, so that a few rows still use every SM. A
+// CTA's part of one list is a segment: an item whose unnormalised softmax is finished here and
+// whose rows are merged with the list's other segments, and with the sequences' own keys, by
+// prefix_merge_kernel. Segment (list, CTA) has slot list + CTA: both grow along the lists, and one of
+// them does from each segment to the next, so slots are distinct and below lists + CTAs.
+
+__device__ __forceinline__ int prefix_length(const Params &p) { return min(max(__ldg(p.seq_lens), 0), p.cap); }
+
+__device__ __forceinline__ long long segment_begin(long long total, int c, int ctas) { return total * c / ctas; }
+
+// List of this CTA's r-th segment, or -1.
+__device__ __forceinline__ int segment_index(const Params &p, int r)
+{
+    const int tiles = (prefix_length(p) + kBN - 1) / kBN;
+    const int lists = p.heads * p.tile_pairs;
+    const long long total = static_cast<long long>(lists) * tiles;
+    const int ctas = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
+    const long long g0 = segment_begin(total, c, ctas), g1 = segment_begin(total, c + 1, ctas);
+    if (g0 >= g1)
+        return -1;
+    const long long list = g0 / tiles + r;
+    return list * tiles < g1 ? static_cast<int>(list) : -1;
+}
+
+__device__ __forceinline__ Item decode_segment(const Params &p, int list)
+{
+    Item it;
+    it.skv = prefix_length(p);
+    it.off = 0;
+    it.b = 0;
+    const int tiles = (it.skv + kBN - 1) / kBN;
+    const long long total = static_cast<long long>(p.heads) * p.tile_pairs * tiles;
+    const int ctas = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
+    const long long g0 = segment_begin(total, c, ctas), g1 = segment_begin(total, c + 1, ctas);
+    const long long first = static_cast<long long>(list) * tiles;
+    it.kt0 = static_cast<int>(max(g0 - first, 0LL));
+    const int n = static_cast<int>(min(g1 - first, static_cast<long long>(tiles))) - it.kt0;
+    it.kvh = list / p.tile_pairs;
+    const int pair = list - it.kvh * p.tile_pairs;
+    it.q0[0] = 2 * pair * p.tile_seqs;
+    it.q0[1] = it.q0[0] + p.tile_seqs;
+    it.hq[0] = it.hq[1] = it.kvh;
+    it.n[0] = n;
+    it.n[1] = it.q0[1] < p.B ? n : 0;
+    it.slot = list + c;
+    return it;
+}
 
 // Work item w, heaviest first (query tiles from the last). With pair_heads (the GQA group is even),
 // tiles A and B are the same 128 query rows of heads 2k and 2k+1, which share a kv head: both need
 // the same number of KV tiles, so they ping-pong to the last one. Otherwise they are two
 // consecutive query tiles of one head, and B needs one KV tile more than A.
-template <bool kPaged>
+template <int kMode>
 __device__ __forceinline__ Item decode_item(const Params &p, int w)
 {
+    if constexpr (kMode == kPrefix)
+        return decode_segment(p, w);
+    constexpr bool kPaged = kMode == kPagedCache;
     const int heads_per_item = p.pair_heads ? 2 : 1;
     const int hpu = p.Hq / heads_per_item;
     int t = w;
@@ -259,6 +329,7 @@ __device__ __forceinline__ Item decode_item(const Params &p, int w)
     }
     const int h_a = hu * heads_per_item;
     Item it;
+    it.kt0 = it.slot = 0;
     it.q0[0] = p.pair_heads ? item * kBM : item * 2 * kBM;
     it.q0[1] = p.pair_heads ? it.q0[0] : it.q0[0] + kBM;
     it.hq[0] = h_a;
@@ -277,25 +348,35 @@ __device__ __forceinline__ Item decode_item(const Params &p, int w)
     return it;
 }
 
+// This CTA's r-th work item: an index into the item list, or the list of KV tiles that a shared-prefix
+// segment belongs to.
+template <int kMode>
+__device__ __forceinline__ int next_work(const Params &p, int r)
+{
+    return kMode == kPrefix ? segment_index(p, r) : work_index(p, r);
+}
+
 // The first of this CTA's items from the r-th on that has a KV tile to stream, or -1. Without a
 // paged cache every item has one; with it, an item whose rows see no key at all is written by the
 // softmax warps alone (O = 0, LSE = -inf) and the producer and the MMA issuer skip it.
-template <bool kPaged>
+template <int kMode>
 __device__ __forceinline__ int next_active(const Params &p, int r)
 {
     for (;; ++r) {
-        const int w = work_index(p, r);
-        if (w < 0 || !kPaged || decode_item<kPaged>(p, w).n_max() > 0)
+        const int w = next_work<kMode>(p, r);
+        if (w < 0 || kMode != kPagedCache || decode_item<kMode>(p, w).n_max() > 0)
             return w < 0 ? -1 : r;
     }
 }
 
-template <int D, bool kPaged>
+template <int D, int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o, const Params p)
 {
     using C = Cfg<D>;
+    constexpr bool kPaged = kMode == kPagedCache;  // per-sequence lengths; rows may see no key
+    constexpr bool kPages = kMode != kDense;       // K and V in pages
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t s_base = smem_u32(smem);
@@ -347,6 +428,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             s_pair_order[rank] = static_cast<uint16_t>(e);
         }
     }
+    if constexpr (kMode == kPrefix) {
+        // The rows behind a tile's last sequence are no TMA box's: zeros, so that their scores are finite.
+        const int used = p.tile_seqs * p.group;
+        for (int i = threadIdx.x; i < 2 * C::kChunks * (kBM - used) * 8; i += kThreads) {
+            const int u = i & 7, row = used + (i >> 3) % (kBM - used), c = (i >> 3) / (kBM - used);
+            *reinterpret_cast<uint4 *>(smem + C::kOffQ + c * C::kChunkBytes + row * 128 + u * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        for (int i = blockIdx.x * kThreads + threadIdx.x; i < p.n_counters; i += gridDim.x * kThreads)
+            p.counters[i] = 0;
+    }
     if (warp == kWarpTma && lane == 0) {
         tma_prefetch_desc(&tm_q);
         tma_prefetch_desc(&tm_k);
@@ -376,20 +468,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             int q_issued = 0;  // Q loads issued so far (one per item with a KV tile)
             bool ok = true;
             int pg[8], ip[8];  // paged: page and first slot of each box of the current KV tile
-            for (int k = next_active<kPaged>(p, 0); ok && k >= 0; k = next_active<kPaged>(p, k + 1)) {
-                const Item it = decode_item<kPaged>(p, work_index(p, k));
+            for (int k = next_active<kMode>(p, 0); ok && k >= 0; k = next_active<kMode>(p, k + 1)) {
+                const Item it = decode_item<kMode>(p, next_work<kMode>(p, k));
                 if (q_issued > 0 && !(ok = mbar_wait(BAR(kBarQFree), static_cast<uint32_t>(q_issued - 1) & 1u,
                                                      abort_flag, p.status, kSitePrefillTmaEmpty)))
                     break;
                 const int n_q = (it.n[1] > 0) ? 2 : 1;
-                mbar_arrive_expect_tx(BAR(kBarQFull), n_q * C::kTileBytes);
+                // Shared prefix: a (dim, head of the group, sequence, kv head) map, whose boxes lay the rows
+                // (sequence, head) of tile_seqs sequences one behind the other; zeros behind the batch.
+                mbar_arrive_expect_tx(BAR(kBarQFull), kMode == kPrefix
+                                                          ? n_q * C::kChunks * p.tile_seqs * p.group * C::kSwizzleBytes
+                                                          : n_q * C::kTileBytes);
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
                     if (x < n_q)
 #pragma unroll
                         for (int c = 0; c < C::kChunks; ++c)
                             tma_load_4d(sQ + x * C::kTileBytes + c * C::kChunkBytes, &tm_q, BAR(kBarQFull),
-                                        c * C::kChunkElems, it.q0[x], it.hq[x], it.b);
+                                        c * C::kChunkElems, kMode == kPrefix ? 0 : it.q0[x],
+                                        kMode == kPrefix ? it.q0[x] : it.hq[x], kMode == kPrefix ? it.kvh : it.b);
                 ++q_issued;
                 const int n_loads = 2 * it.n_max();  // K0, V0, K1, V1, ...
                 for (int i = 0; i < n_loads; ++i, ++kv) {
@@ -400,14 +497,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive_expect_tx(BAR(kBarFull0 + slot), C::kTileBytes);
                     const CUtensorMap *map = (i & 1) ? &tm_v : &tm_k;
                     const uint32_t dst = sRing + slot * C::kTileBytes;
-                    if constexpr (kPaged) {
+                    if constexpr (kPages) {
                         // The tile's keys come page by page, in boxes of min(page_size, 128) rows. A
                         // box past the sequence's length, or whose block-table entry lies outside
                         // [0, num_pages), reads the page beyond the last one: zeros.
                         const int rows = min(p.page_size, kBN);
                         const int n_box = kBN / rows;
                         if ((i & 1) == 0) {  // K: look the pages up; V reuses them
-                            const int k0 = (i >> 1) * kBN;
+                            const int k0 = (it.kt0 + (i >> 1)) * kBN;
 #pragma unroll
                             for (int l = 0; l < 8; ++l) {
                                 const int key = k0 + l * rows;
@@ -428,8 +525,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                                 for (int c = 0; c < C::kChunks; ++c)
                                     tma_load_4d_hint(dst + c * C::kChunkBytes + l * rows * C::kSwizzleBytes, map,
-                                                     BAR(kBarFull0 + slot), c * C::kChunkElems, ip[l], it.kvh, pg[l],
-                                                     pol);
+                                                     BAR(kBarFull0 + slot), c * C::kChunkElems, ip[l], kMode == kPrefix ? it.kvh / p.sub_groups : it.kvh,
+                                                     pg[l], pol);
                     } else {
 #pragma unroll
                         for (int c = 0; c < C::kChunks; ++c)
@@ -503,11 +600,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
 
             bool ok = true;
-            int r_cur = next_active<kPaged>(p, 0);  // this CTA's item index (items with KV tiles only)
+            int r_cur = next_active<kMode>(p, 0);  // this CTA's item index (items with KV tiles only)
             Item it{};
             if (r_cur >= 0) {
                 // The first item's S_X(0); every later item's are issued during the item before it.
-                it = decode_item<kPaged>(p, work_index(p, r_cur));
+                it = decode_item<kMode>(p, next_work<kMode>(p, r_cur));
                 ok = mbar_wait(BAR(kBarQFull), 0, abort_flag, p.status, kSitePrefillMmaQ) && wait_kv(0);
                 if (ok) {
                     tc_fence_after_sync();
@@ -522,9 +619,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t kv_base = 0;           // ring position of the current item's K0
             uint32_t p_cnt[2] = {0u, 0u};   // P_X tiles consumed so far (phase of PHalf_X / PFull_X)
             for (int k = 0; ok && r_cur >= 0; ++k) {  // k: Q loads consumed so far (phase of QFull)
-                const int r_next = next_active<kPaged>(p, r_cur + 1);
-                const int w_next = (r_next >= 0) ? work_index(p, r_next) : -1;
-                const Item nx = (w_next >= 0) ? decode_item<kPaged>(p, w_next) : Item{};
+                const int r_next = next_active<kMode>(p, r_cur + 1);
+                const int w_next = (r_next >= 0) ? next_work<kMode>(p, r_next) : -1;
+                const Item nx = (w_next >= 0) ? decode_item<kMode>(p, w_next) : Item{};
                 const uint32_t kv_next = kv_base + 2u * static_cast<uint32_t>(it.n_max());  // next item's K0
                 // The Q tiles may be replaced once every S product of this item has been issued (and,
                 // by the commit, completed): the last S_X is S_X(n_X - 1), issued at j = n_X - 2.
@@ -581,11 +678,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = flush_next(false);
                 for (int j = 0; ok && j < it.n_max(); ++j) {
                     const uint32_t item_v = kv_base + 2u * j + 1u, item_k = kv_base + 2u * j + 2u;
-                    if constexpr (kPaged) {
+                    if constexpr (kPages) {
                         // Rows of V_j past the sequence's length hold whatever the cache holds in the
                         // last page's unused slots; their weights are 0, but 0 * NaN is not: zero them
                         // before the first PV product reads the tile.
-                        const int r0 = it.skv - j * kBN;
+                        const int r0 = it.skv - (it.kt0 + j) * kBN;
                         if (r0 < kBN) {
                             if (!(ok = wait_kv(item_v)))
                                 break;
@@ -668,10 +765,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the last PV product (the integer divisions of a decode cost ~0.5 us of issue here), so the
         // next item's softmax starts right after the epilogue.
         struct Tile {
-            int n = 0, q0 = 0, skv = 0, off = 0, hq = 0, b = 0;
+            int n = 0, q0 = 0, skv = 0, off = 0, hq = 0, b = 0, kt0 = 0, slot = 0;
         };
         auto tile_of = [&](int w) {
-            const Item it = decode_item<kPaged>(p, w);
+            const Item it = decode_item<kMode>(p, w);
             Tile t;
             t.n = x ? it.n[1] : it.n[0];
             t.q0 = x ? it.q0[1] : it.q0[0];
@@ -679,14 +776,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             t.off = it.off;
             t.hq = x ? it.hq[1] : it.hq[0];
             t.b = it.b;
+            if constexpr (kMode == kPrefix) {
+                t.kt0 = it.kt0;
+                t.slot = it.slot;
+            }
             return t;
         };
-        int w = work_index(p, 0);
+        int w = next_work<kMode>(p, 0);
         Tile cur = (w >= 0) ? tile_of(w) : Tile{};
         Tile nxt{};
         int w_next = -1;
         for (int k = 0; ok && w >= 0; ++k, w = w_next, cur = nxt) {
-            w_next = work_index(p, k + 1);
+            w_next = next_work<kMode>(p, k + 1);
             const int n = cur.n, q0 = cur.q0, skv = cur.skv, off = cur.off;
             const int row = q0 + r;
             if (kPaged && n == 0 && q0 < p.Sq) {
@@ -720,11 +821,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < kBN; ++c)
                     s[c] = __uint_as_float(s_raw[c]);
 
-                const int k0 = j * kBN;
-                const bool need_mask = (k0 + kBN > skv) || (p.causal && k0 + kBN - 1 > q0 + off);
+                const int k0 = (cur.kt0 + j) * kBN;
+                const bool need_mask = (k0 + kBN > skv) || (kMode != kPrefix && p.causal && k0 + kBN - 1 > q0 + off);
                 if (need_mask) {
                     int limit = skv - 1 - k0;  // last visible column of this tile for this row
-                    if (p.causal)
+                    if (kMode != kPrefix && p.causal)
                         limit = min(limit, row + off - k0);
 #pragma unroll
                     for (int c = 0; c < kBN; ++c)
@@ -821,6 +922,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after_sync();
             // Paged: a row that saw no key has l = 0: O = 0 and LSE = m + log2(0) = -inf.
             const float inv_l = (kPaged && !(l_pv > 0.f)) ? 0.f : 1.f / l_pv;
+            if constexpr (kMode == kPrefix) {
+                // Partials: normalised O in fp32, 32 dims at a time through the warp's staging box (as the
+                // bf16 O below), and the LSE in log2 units. Rows behind the last sequence are written too
+                // (the slot has room for every row) and never read.
+                const uint32_t wstage = s_base + C::kOffStage + static_cast<uint32_t>(warp) * C::kWarpStageBytes;
+                uint8_t *wrow = smem + C::kOffStage + warp * C::kWarpStageBytes + lane * 128;
+                const int row0 = (cur.slot * 2 + x) * kBM + 32 * (warp & 3);
+#pragma unroll 1
+                for (int h = 0; h < D / 32; ++h) {
+                    uint32_t ov[32];
+                    tmem_ld32_wait(tO + h * 32, ov);
+                    if (lane == 0)
+                        bulk_wait_group_read0();
+                    __syncwarp();
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        *reinterpret_cast<float4 *>(wrow + ((u ^ (lane & 7)) << 4)) =
+                            make_float4(__uint_as_float(ov[4 * u]) * inv_l, __uint_as_float(ov[4 * u + 1]) * inv_l,
+                                        __uint_as_float(ov[4 * u + 2]) * inv_l, __uint_as_float(ov[4 * u + 3]) * inv_l);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && 32 * (warp & 3) < p.tile_seqs * p.group) {
+                        tma_store_4d(&tm_o, wstage, h * 32, row0, 0, 0);
+                        bulk_commit_group();
+                    }
+                }
+                p.part_lse[row0 + lane] = m + log2f(l);
+                tc_fence_before_sync();
+                continue;
+            }
             const bool store = row < p.Sq;
             const int hq = cur.hq;
             const size_t bh_q = static_cast<size_t>(cur.b) * p.Hq + hq;
@@ -896,9 +1027,51 @@ __global__ void __launch_bounds__(kThreads, 1)
 #undef BAR
 }
 
-template <int D, bool kPaged>
+// The partials of a shared prefix: fp32 [rows][128], stored in boxes of 32 dims x 32 rows.
+bool make_map_partials(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap *map, float *base, long long rows, int *err)
+{
+    const cuuint64_t dims[4] = {128, static_cast<cuuint64_t>(rows), 1, 1};
+    const cuuint64_t strides[3] = {512, static_cast<cuuint64_t>(rows) * 512, static_cast<cuuint64_t>(rows) * 512};
+    const cuuint32_t box[4] = {32, 32, 1, 1}, estr[4] = {1, 1, 1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, base, dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        *err = static_cast<int>(r);
+    return r == CUDA_SUCCESS;
+}
+
+// Sets an instantiation's attributes on the current device once.
+template <int D, int kMode>
+cudaError_t prepare()
+{
+    using C = Cfg<D>;
+    // Per device: the attribute applies to the device current when it is set (benign race between
+    // host threads: every caller sets the same value).
+    static bool attr_set[kMaxDevices] = {};
+    const int dev = current_device_index();
+    if (dev < 0)
+        return cudaErrorInvalidDevice;
+    if (attr_set[dev])
+        return cudaSuccess;
+    // The setmaxnreg split inside the kernel is only valid for the register count it was
+    // written for; refuse to launch a build that was compiled to anything else.
+    cudaFuncAttributes fa;
+    cudaError_t e = cudaFuncGetAttributes(&fa, prefill_kernel<D, kMode>);
+    if (e != cudaSuccess)
+        return e;
+    if (fa.numRegs != kLaunchRegs)
+        return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(prefill_kernel<D, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e == cudaSuccess)
+        attr_set[dev] = true;
+    return e;
+}
+
+template <int D, int kMode>
 cudaError_t launch(const PrefillArgs &a, cudaStream_t stream, int *encode_error)
 {
+    constexpr bool kPaged = kMode == kPagedCache;
     using C = Cfg<D>;
     auto encode = get_encode_fn();
     if (!encode) {
@@ -934,26 +1107,9 @@ cudaError_t launch(const PrefillArgs &a, cudaStream_t stream, int *encode_error)
             return cudaErrorInvalidValue;
     }
 
-    // Per device: the attribute applies to the device current when it is set (benign race between
-    // host threads: every caller sets the same value).
-    static bool attr_set[kMaxDevices] = {};
-    const int dev = current_device_index();
-    if (dev < 0)
-        return cudaErrorInvalidDevice;
-    if (!attr_set[dev]) {
-        // The setmaxnreg split inside the kernel is only valid for the register count it was
-        // written for; refuse to launch a build that was compiled to anything else.
-        cudaFuncAttributes fa;
-        cudaError_t e = cudaFuncGetAttributes(&fa, prefill_kernel<D, kPaged>);
-        if (e != cudaSuccess)
-            return e;
-        if (fa.numRegs != kLaunchRegs)
-            return cudaErrorInvalidConfiguration;
-        e = cudaFuncSetAttribute(prefill_kernel<D, kPaged>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-        if (e != cudaSuccess)
-            return e;
-        attr_set[dev] = true;
-    }
+    const cudaError_t ready = prepare<D, kMode>();
+    if (ready != cudaSuccess)
+        return ready;
     Params p;
     p.o = static_cast<__nv_bfloat16 *>(a.o);
     p.o_sb = a.os.b;
@@ -989,7 +1145,7 @@ cudaError_t launch(const PrefillArgs &a, cudaStream_t stream, int *encode_error)
     p.n_work = static_cast<int>(n_work);
     // Persistent: one CTA per SM (each holds all 512 TMEM columns), never more than the items.
     const int grid = static_cast<int>(n_work < a.sm_count ? n_work : a.sm_count);
-    prefill_kernel<D, kPaged><<<static_cast<unsigned>(grid), kThreads, C::kSmem, stream>>>(tq, tk, tv, to, p);
+    prefill_kernel<D, kMode><<<static_cast<unsigned>(grid), kThreads, C::kSmem, stream>>>(tq, tk, tv, to, p);
     return cudaGetLastError();
 }
 
@@ -999,17 +1155,100 @@ cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream, int *encod
 {
     *encode_error = 0;
     if (a.seq_lens)  // paged, variable-length cache: head dim 128
-        return a.D == 128 ? launch<128, true>(a, stream, encode_error) : cudaErrorInvalidValue;
+        return a.D == 128 ? launch<128, kPagedCache>(a, stream, encode_error) : cudaErrorInvalidValue;
     switch (a.D) {
     case 32:
-        return launch<32, false>(a, stream, encode_error);
+        return launch<32, kDense>(a, stream, encode_error);
     case 64:
-        return launch<64, false>(a, stream, encode_error);
+        return launch<64, kDense>(a, stream, encode_error);
     case 128:
-        return launch<128, false>(a, stream, encode_error);
+        return launch<128, kDense>(a, stream, encode_error);
     default:
         return cudaErrorInvalidValue;
     }
+}
+
+PrefixPlan prefix_plan(int B, int Hq, int Hkv, int max_prefix_len, int sm_count)
+{
+    PrefixPlan pl;
+    // A tile holds whole groups of query heads; a group above 128 heads goes in equal parts.
+    int group = Hq / Hkv, sub = 1;
+    while (group / sub > kBM || group % sub != 0)
+        ++sub;
+    pl.sub_groups = sub;
+    pl.group = group / sub;
+    pl.tile_seqs = kBM / pl.group;
+    const int tiles = (B + pl.tile_seqs - 1) / pl.tile_seqs;
+    pl.tile_pairs = (tiles + 1) / 2;
+    pl.lists = static_cast<long long>(Hkv) * sub * pl.tile_pairs;
+    const long long units = pl.lists * ((static_cast<long long>(max_prefix_len) + kBN - 1) / kBN);
+    pl.ctas = static_cast<int>(units < 1 ? 1 : units < sm_count ? units : sm_count);
+    pl.slots = pl.lists + pl.ctas;
+    return pl;
+}
+
+cudaError_t launch_prefix(const PrefixArgs &a, cudaStream_t stream, int *encode_error)
+{
+    constexpr int D = 128;
+    using C = Cfg<D>;
+    *encode_error = 0;
+    auto encode = get_encode_fn();
+    if (!encode) {
+        *encode_error = -1;
+        return cudaErrorInitializationError;
+    }
+    const PrefixPlan &pl = a.plan;
+    CUtensorMap tq, tk, tv, to;
+    // q as (dim, head of the group, sequence, kv head): boxes of 64 dims, a group, tile_seqs sequences.
+    {
+        const cuuint64_t dims[4] = {D, static_cast<cuuint64_t>(pl.group), static_cast<cuuint64_t>(a.B),
+                                    static_cast<cuuint64_t>(a.Hq / pl.group)};
+        const cuuint64_t strides[3] = {D * 2, static_cast<cuuint64_t>(a.Hq) * D * 2, static_cast<cuuint64_t>(pl.group) * D * 2};
+        const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(pl.group), static_cast<cuuint32_t>(pl.tile_seqs), 1};
+        const cuuint32_t estr[4] = {1, 1, 1, 1};
+        const CUresult r = encode(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(a.q), dims, strides, box, estr,
+                                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        if (r != CUDA_SUCCESS) {
+            *encode_error = static_cast<int>(r);
+            return cudaErrorInvalidValue;
+        }
+    }
+    const Strides pst{static_cast<long long>(a.Hkv) * a.page_size * D, static_cast<long long>(a.page_size) * D, D};
+    const int rows = a.page_size < kBN ? a.page_size : kBN;
+    if (!make_map4(encode, &tk, a.k_pages, 2, D, a.page_size, a.Hkv, a.num_pages, pst, 64, rows, CU_TENSOR_MAP_SWIZZLE_128B,
+                   encode_error) ||
+        !make_map4(encode, &tv, a.v_pages, 2, D, a.page_size, a.Hkv, a.num_pages, pst, 64, rows, CU_TENSOR_MAP_SWIZZLE_128B,
+                   encode_error) ||
+        !make_map_partials(encode, &to, a.part_o, static_cast<long long>(pl.slots) * 2 * kBM, encode_error))
+        return cudaErrorInvalidValue;
+    const cudaError_t ready = prepare<D, kPrefix>();
+    if (ready != cudaSuccess)
+        return ready;
+    Params p{};
+    p.status = a.status;
+    p.B = a.B;
+    p.Hq = a.Hq;
+    p.Hkv = a.Hkv;
+    p.Sq = 1;
+    p.group = pl.group;
+    p.sub_groups = pl.sub_groups;
+    p.heads = a.Hkv * pl.sub_groups;
+    p.tile_seqs = pl.tile_seqs;
+    p.tile_pairs = pl.tile_pairs;
+    p.scale_log2 = a.scale * kLog2e;
+    p.seq_lens = a.prefix_len;
+    p.block_table = a.prefix_table;
+    p.num_pages = a.num_pages;
+    p.page_size = a.page_size;
+    p.pages_per_seq = a.prefix_pages;
+    const long long cap = static_cast<long long>(a.prefix_pages) * a.page_size;
+    p.cap = static_cast<int>(cap < a.max_prefix_len ? cap : a.max_prefix_len);
+    p.part_lse = a.part_lse;
+    p.counters = a.counters;
+    p.n_counters = a.n_counters;
+    prefill_kernel<D, kPrefix><<<static_cast<unsigned>(pl.ctas), kThreads, C::kSmem, stream>>>(tq, tk, tv, to, p);
+    return cudaGetLastError();
 }
 
 }  // namespace attn_b200

@@ -156,8 +156,8 @@ int attn_version(void);
 
 /*
  * attn_device_status — synchronises `stream`, then reads and clears the current device's status
- * words: the workspace's (every entry point except attn_decode_noalloc) and, once
- * attn_decode_noalloc has run on the device, the one in its fixed array. Returns ATTN_OK if no
+ * words: the workspace's (every entry point except attn_decode_noalloc and attn_decode_prefix) and,
+ * once attn_decode_noalloc or attn_decode_prefix has run on the device, those entry points' own. Returns ATTN_OK if no
  * kernel-side wait has run out since the last call,
  * ATTN_ERR_DEVICE_TIMEOUT if one has, or ATTN_ERR_CUDA if the stream could not be synchronised.
  * This is a diagnostic call: it blocks the host, so it does not belong on a hot path.
@@ -462,6 +462,47 @@ int attn_append_paged_fp8(const void *q, const void *k, const void *v, const voi
                           const long long *q_strides, const long long *k_strides, const long long *v_strides,
                           const long long *q_out_strides, int num_pages, int page_size, int pages_per_seq, int rot_dim,
                           int max_pos, int interleaved, float eps, void *stream);
+
+/*
+ * attn_decode_prefix — single-token decode (Sq == 1) for a batch whose sequences all start with the
+ * same prefix: sequence b's new token attends to the prefix's keys and to its own suffix's,
+ *   o_b = softmax over { prefix keys 0 .. prefix_len - 1 } and { suffix keys 0 .. len_b - 1 }.
+ * The result is attn_decode_paged's over the concatenated keys, but the prefix is held once and read
+ * once for the whole batch: the batch's query heads of one kv head are the rows of one matrix product.
+ *
+ * Source (page title, section): partial results over disjoint keys combine through their LSEs — "AI
+ * Infra 入门…", §3 (LSE paragraph); query heads sharing a K/V head — "05 · Tích vô hướng…", §4, here
+ * taken across the batch as well. The prefix and its table are this library's choice.
+ *
+ *   q, o, lse        as attn_decode_paged.
+ *   k_pages, v_pages, num_pages, page_size   the cache that holds prefix and suffixes, as
+ *                    attn_decode_paged.
+ *   prefix_table     int32 [prefix_pages] on the device: the prefix's n-th page_size keys live in page
+ *                    prefix_table[n].
+ *   prefix_len       int32 [1] on the device; clamped to [0, min(max_prefix_len, prefix_pages *
+ *                    page_size)]. It need not fill its last page.
+ *   block_table, pages_per_seq, seq_lens, max_seq_len   the suffixes, as attn_decode_paged: seq_lens[b]
+ *                    counts sequence b's keys behind the prefix. (Rotated keys take their positions
+ *                    before they are cached: see attn_append_paged's positions.)
+ *   workspace        workspace_bytes >= attn_decode_prefix_workspace(...) bytes on the device, 256-byte
+ *                    aligned, owned by the caller and used only until the call's work is done; its
+ *                    contents need not be kept or cleared. Calls that overlap need one each; a captured
+ *                    call keeps using the one it was given.
+ * A sequence with neither prefix nor suffix keys gets o = 0 and lse = -inf. Table entries outside
+ * [0, num_pages) read as zeros. bf16 cache, head dim 128, 1 <= B <= 1024, B * Hq <= 2^22, Hq % Hkv == 0.
+ * Lengths and tables are read on the device, never on the host. Never allocates or synchronises; the
+ * first call on a device comes before any stream capture. Returns ATTN_OK or a negative attn_status
+ * (argument errors before any launch; ATTN_ERR_WORKSPACE when the workspace is too small).
+ */
+int attn_decode_prefix(const void *q, const void *k_pages, const void *v_pages, const int *prefix_table,
+                       const int *prefix_len, const int *block_table, const int *seq_lens, void *o, float *lse,
+                       void *workspace, long long workspace_bytes, int B, int Hq, int Hkv, int num_pages,
+                       int page_size, int prefix_pages, int max_prefix_len, int pages_per_seq, int max_seq_len,
+                       float scale, void *stream);
+
+/* attn_decode_prefix_workspace — bytes of workspace that attn_decode_prefix needs for these sizes on the
+ * current device (it grows with each of them), or a negative attn_status. */
+long long attn_decode_prefix_workspace(int B, int Hq, int Hkv, int max_prefix_len, int max_seq_len);
 
 #ifdef __cplusplus
 }

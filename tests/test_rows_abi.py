@@ -136,3 +136,40 @@ def test_binding_rejects_cpu_tensors_and_wrong_types():
         attn.attn_append_paged(q.half(), q, None, None, q, q, q, q)
     with pytest.raises(TypeError, match="k_scale"):
         attn.attn_append_paged_fp8(q, q, None, None, q, q, None, None, q, q)
+
+
+def prefix(lib, **kw):
+    names = ("q", "kp", "vp", "ptab", "plen", "tab", "lens", "o", "lse", "ws")
+    p = dict(zip(names, A))
+    a = dict(ws_bytes=1 << 40, B=2, Hq=8, Hkv=2, num_pages=9, page=64, prefix_pages=3, max_prefix=150, per=2, max_seq=100,
+             scale=0.1)
+    for d in (p, a):
+        d.update({k: v for k, v in kw.items() if k in d})
+    return lib.attn_decode_prefix(*p.values(), *a.values(), None)
+
+
+@pytest.mark.parametrize("name,over,expected", [
+    ("null prefix table", dict(ptab=None), -1),
+    ("null prefix length", dict(plen=None), -1),
+    ("null workspace", dict(ws=None), -1),
+    ("batch 1025", dict(B=1025), -2),
+    ("too many rows", dict(B=1024, Hq=8192, Hkv=1), -2),
+    ("negative bound", dict(max_prefix=-1), -2),
+    ("no prefix pages", dict(prefix_pages=0), -2),
+    ("page size 80", dict(page=80), -2),
+    ("pages past 32 bits", dict(num_pages=1 << 30), -2),
+    ("prefix past 32 bits", dict(prefix_pages=1 << 26), -2),
+    ("gqa not divisible", dict(Hq=7), -3),
+    ("misaligned workspace", dict(ws=A[9] + 16), -5),
+    ("misaligned lse", dict(lse=A[8] + 4), -5),
+    ("misaligned prefix length", dict(plen=A[4] + 2), -5),
+    ("nan scale", dict(scale=float("nan")), -11),
+])
+def test_prefix_argument_errors(lib, name, over, expected):
+    assert prefix(lib, **over) == expected, name
+
+
+def test_prefix_workspace_argument_errors(lib):
+    assert lib.attn_decode_prefix_workspace(0, 8, 2, 10, 10) == -2
+    assert lib.attn_decode_prefix_workspace(2, 7, 2, 10, 10) == -3
+    assert lib.attn_decode_prefix_workspace(2, 8, 2, 10, -1) == -2
