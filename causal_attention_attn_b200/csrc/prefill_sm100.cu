@@ -462,71 +462,93 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------------------------------------------------------- TMA producer
         // Per item: Q_A (and Q_B) once the previous item's last S products have read the Q tiles,
         // then K0, V0, K1, V1, ... through the ring, whose position runs on across items.
-        if (lane == 0) {
+        // Pages: the whole warp walks the schedule, lane l holding the l-th box of a tile (its
+        // block-table entry is looked up while the tile before it is on its way); otherwise lane 0 alone.
+        if (kPages || lane == 0) {
+            const bool issuer = lane == 0;
             const uint64_t pol = l2_policy_evict_last();  // K/V tiles are re-read by sibling CTAs
             uint32_t kv = 0;   // K/V loads issued so far
             int q_issued = 0;  // Q loads issued so far (one per item with a KV tile)
             bool ok = true;
-            int pg[8], ip[8];  // paged: page and first slot of each box of the current KV tile
+            auto wait = [&](int bar, uint32_t parity) {
+                const bool r = mbar_wait(BAR(bar), parity, abort_flag, p.status, kSitePrefillTmaEmpty);
+                return kPages ? __all_sync(0xffffffffu, r) != 0 : r;
+            };
+            // A tile's keys come page by page, in boxes of min(page_size, 128) rows; a tile starts at a
+            // page's start or, in larger pages, at a multiple of 128 in one.
+            const int rows = kPages ? min(p.page_size, kBN) : kBN;
+            const int n_box = kBN / rows;
             for (int k = next_active<kMode>(p, 0); ok && k >= 0; k = next_active<kMode>(p, k + 1)) {
                 const Item it = decode_item<kMode>(p, next_work<kMode>(p, k));
-                if (q_issued > 0 && !(ok = mbar_wait(BAR(kBarQFree), static_cast<uint32_t>(q_issued - 1) & 1u,
-                                                     abort_flag, p.status, kSitePrefillTmaEmpty)))
+                if (q_issued > 0 && !(ok = wait(kBarQFree, static_cast<uint32_t>(q_issued - 1) & 1u)))
                     break;
                 const int n_q = (it.n[1] > 0) ? 2 : 1;
                 // Shared prefix: a (dim, head of the group, sequence, kv head) map, whose boxes lay the rows
                 // (sequence, head) of tile_seqs sequences one behind the other; zeros behind the batch.
-                mbar_arrive_expect_tx(BAR(kBarQFull), kMode == kPrefix
-                                                          ? n_q * C::kChunks * p.tile_seqs * p.group * C::kSwizzleBytes
-                                                          : n_q * C::kTileBytes);
+                if (issuer) {
+                    mbar_arrive_expect_tx(BAR(kBarQFull), kMode == kPrefix
+                                                              ? n_q * C::kChunks * p.tile_seqs * p.group * C::kSwizzleBytes
+                                                              : n_q * C::kTileBytes);
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
-                    if (x < n_q)
+                    for (int x = 0; x < 2; ++x)
+                        if (x < n_q)
 #pragma unroll
-                        for (int c = 0; c < C::kChunks; ++c)
-                            tma_load_4d(sQ + x * C::kTileBytes + c * C::kChunkBytes, &tm_q, BAR(kBarQFull),
-                                        c * C::kChunkElems, kMode == kPrefix ? 0 : it.q0[x],
-                                        kMode == kPrefix ? it.q0[x] : it.hq[x], kMode == kPrefix ? it.kvh : it.b);
+                            for (int c = 0; c < C::kChunks; ++c)
+                                tma_load_4d(sQ + x * C::kTileBytes + c * C::kChunkBytes, &tm_q, BAR(kBarQFull),
+                                            c * C::kChunkElems, kMode == kPrefix ? 0 : it.q0[x],
+                                            kMode == kPrefix ? it.q0[x] : it.hq[x], kMode == kPrefix ? it.kvh : it.b);
+                }
                 ++q_issued;
                 const int n_loads = 2 * it.n_max();  // K0, V0, K1, V1, ...
+                const int kvh = kMode == kPrefix ? it.kvh / p.sub_groups : it.kvh;
+                // This lane's box of the current tile: first key, block-table entry, first slot in the page.
+                int key = 0, entry = 0, in_page = 0, page = 0;
+                auto look_up = [&]() {
+                    // Past the length, or an entry outside [0, num_pages): the page beyond the last, zeros.
+                    int pg = p.num_pages;
+                    if (lane < n_box && key < it.skv) {
+                        pg = __ldg(p.block_table + static_cast<size_t>(it.b) * p.pages_per_seq + entry);
+                        if (pg < 0 || pg >= p.num_pages)
+                            pg = p.num_pages;
+                    }
+                    return pg;
+                };
+                int next_page = 0;
+                if constexpr (kPages) {
+                    key = it.kt0 * kBN + lane * rows;
+                    entry = key / p.page_size;
+                    in_page = key - entry * p.page_size;
+                    next_page = look_up();
+                }
                 for (int i = 0; i < n_loads; ++i, ++kv) {
                     const uint32_t slot = kv % kRing;
-                    if (!(ok = mbar_wait(BAR(kBarEmpty0 + slot), ((kv / kRing) & 1u) ^ 1u, abort_flag, p.status,
-                                         kSitePrefillTmaEmpty)))
+                    if (!(ok = wait(kBarEmpty0 + slot, ((kv / kRing) & 1u) ^ 1u)))
                         break;
-                    mbar_arrive_expect_tx(BAR(kBarFull0 + slot), C::kTileBytes);
+                    if (issuer)
+                        mbar_arrive_expect_tx(BAR(kBarFull0 + slot), C::kTileBytes);
                     const CUtensorMap *map = (i & 1) ? &tm_v : &tm_k;
                     const uint32_t dst = sRing + slot * C::kTileBytes;
                     if constexpr (kPages) {
-                        // The tile's keys come page by page, in boxes of min(page_size, 128) rows. A
-                        // box past the sequence's length, or whose block-table entry lies outside
-                        // [0, num_pages), reads the page beyond the last one: zeros.
-                        const int rows = min(p.page_size, kBN);
-                        const int n_box = kBN / rows;
-                        if ((i & 1) == 0) {  // K: look the pages up; V reuses them
-                            const int k0 = (it.kt0 + (i >> 1)) * kBN;
+                        if ((i & 1) == 0)
+                            page = next_page;
+                        if (lane < n_box) {
 #pragma unroll
-                            for (int l = 0; l < 8; ++l) {
-                                const int key = k0 + l * rows;
-                                int page = p.num_pages;
-                                if (l < n_box && key < it.skv) {
-                                    page = __ldg(p.block_table + static_cast<size_t>(it.b) * p.pages_per_seq +
-                                                 key / p.page_size);
-                                    if (page < 0 || page >= p.num_pages)
-                                        page = p.num_pages;
-                                }
-                                pg[l] = page;
-                                ip[l] = key % p.page_size;
-                            }
+                            for (int c = 0; c < C::kChunks; ++c)
+                                tma_load_4d_hint(dst + c * C::kChunkBytes + lane * rows * C::kSwizzleBytes, map,
+                                                 BAR(kBarFull0 + slot), c * C::kChunkElems, in_page, kvh, page, pol);
                         }
-#pragma unroll
-                        for (int l = 0; l < 8; ++l)
-                            if (l < n_box)
-#pragma unroll
-                                for (int c = 0; c < C::kChunks; ++c)
-                                    tma_load_4d_hint(dst + c * C::kChunkBytes + l * rows * C::kSwizzleBytes, map,
-                                                     BAR(kBarFull0 + slot), c * C::kChunkElems, ip[l], kMode == kPrefix ? it.kvh / p.sub_groups : it.kvh,
-                                                     pg[l], pol);
+                        if (i & 1) {  // on to the next tile: 128 keys, that is n_box pages or a part of one
+                            key += kBN;
+                            in_page += kBN;
+                            if (n_box > 1) {
+                                entry += n_box;
+                                in_page = 0;
+                            } else if (in_page >= p.page_size) {
+                                ++entry;
+                                in_page = 0;
+                            }
+                            next_page = look_up();
+                        }
                     } else {
 #pragma unroll
                         for (int c = 0; c < C::kChunks; ++c)
@@ -535,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (*abort_flag) {
+            if (*abort_flag && issuer) {
                 // Let every copy already issued land before the CTA exits.
                 if (q_issued > 0)
                     mbar_wait_drain(BAR(kBarQFull), static_cast<uint32_t>(q_issued - 1) & 1u, 100000000ull);
