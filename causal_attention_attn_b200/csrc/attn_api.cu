@@ -738,7 +738,7 @@ namespace {
 
 // attn_decode_prefix's workspace, cut up.
 struct PrefixSpace {
-    size_t counters, suffix_ws, o_suffix, lse_suffix, part_o, part_lse, bytes;  // byte offsets
+    size_t suffix_ws, o_suffix, lse_suffix, part_o, part_lse, bytes;  // byte offsets
 };
 
 PrefixSpace prefix_space(int B, int Hq, const PrefixPlan &pl, const DecodePlan &suffix)
@@ -751,7 +751,6 @@ PrefixSpace prefix_space(int B, int Hq, const PrefixPlan &pl, const DecodePlan &
     };
     PrefixSpace sp;
     const size_t rows = static_cast<size_t>(B) * Hq;
-    sp.counters = take(static_cast<size_t>(suffix.pairs) * sizeof(int));
     sp.suffix_ws = take(suffix.partial_floats * sizeof(float));
     sp.o_suffix = take(rows * 128 * sizeof(float));
     sp.lse_suffix = take(rows * sizeof(float));
@@ -778,10 +777,8 @@ int plan_prefix(const DeviceState &s, int B, int Hq, int Hkv, int max_prefix_len
                 DecodePlan *suffix, PrefixSpace *sp)
 {
     *pl = prefix_plan(B, Hq, Hkv, max_prefix_len, s.sm_count);
-    if (decode_plan_paged(B, Hq, Hkv, max_seq_len, 0, s.sm_count, suffix) != cudaSuccess) {
-        cudaGetLastError();
+    if (decode_plan_suffix(B, Hq, Hkv, max_seq_len, s.sm_count, suffix) != cudaSuccess)
         return ATTN_ERR_SHAPE;
-    }
     if (pl->slots * 256 > INT_MAX)
         return ATTN_ERR_SHAPE;
     *sp = prefix_space(B, Hq, *pl, *suffix);
@@ -856,6 +853,39 @@ extern "C" int attn_decode_prefix(const void *q, const void *k_pages, const void
         s->prefix_status = static_cast<int *>(word);
     }
     auto at = [&](size_t off) { return static_cast<char *>(workspace) + off; };
+    // The suffixes first: the prefix's kernel needs nothing of theirs and starts on the SMs that they
+    // leave free; the merge waits for both.
+    const bool own = max_seq_len > 0;
+    const long long own_cap = static_cast<long long>(pages_per_seq) * page_size;
+    if (own) {
+        DecodeArgs a;
+        a.q = q;
+        a.k = k_pages;
+        a.v = v_pages;
+        a.o = nullptr;
+        a.o_part = reinterpret_cast<float *>(at(sp.o_suffix));
+        a.lse = reinterpret_cast<float *>(at(sp.lse_suffix));
+        a.B = B;
+        a.Hq = Hq;
+        a.Hkv = Hkv;
+        a.Skv = 0;
+        a.D = 128;
+        a.scale = scale;
+        a.plan = suffix;
+        a.ws = reinterpret_cast<float *>(at(sp.suffix_ws));
+        a.counters = nullptr;  // no pair is merged in the kernel
+        a.status = s->prefix_status;
+        a.seq_lens = seq_lens;
+        a.block_table = block_table;
+        a.num_pages = num_pages;
+        a.page_size = page_size;
+        a.pages_per_seq = pages_per_seq;
+        a.max_seq_len = max_seq_len;
+        if (launch_decode_tc(a, stream) != cudaSuccess) {
+            cudaGetLastError();
+            return ATTN_ERR_LAUNCH;
+        }
+    }
     PrefixArgs pa;
     pa.q = q;
     pa.k_pages = k_pages;
@@ -873,48 +903,18 @@ extern "C" int attn_decode_prefix(const void *q, const void *k_pages, const void
     pa.plan = pl;
     pa.part_o = reinterpret_cast<float *>(at(sp.part_o));
     pa.part_lse = reinterpret_cast<float *>(at(sp.part_lse));
-    pa.counters = reinterpret_cast<int *>(at(sp.counters));
-    pa.n_counters = static_cast<int>(suffix.pairs);
     pa.status = s->prefix_status;
+    pa.behind_suffix = own;
     int encode_error = 0;
     if (launch_prefix(pa, stream, &encode_error) != cudaSuccess) {
         cudaGetLastError();
         return encode_error ? ATTN_ERR_CUDA : ATTN_ERR_LAUNCH;
     }
-    const bool own = max_seq_len > 0;
-    if (own) {
-        DecodeArgs a;
-        a.q = q;
-        a.k = k_pages;
-        a.v = v_pages;
-        a.o = nullptr;
-        a.o_part = reinterpret_cast<float *>(at(sp.o_suffix));
-        a.lse = reinterpret_cast<float *>(at(sp.lse_suffix));
-        a.B = B;
-        a.Hq = Hq;
-        a.Hkv = Hkv;
-        a.Skv = 0;
-        a.D = 128;
-        a.scale = scale;
-        a.plan = suffix;
-        a.ws = reinterpret_cast<float *>(at(sp.suffix_ws));
-        a.counters = pa.counters;
-        a.status = s->prefix_status;
-        a.seq_lens = seq_lens;
-        a.block_table = block_table;
-        a.num_pages = num_pages;
-        a.page_size = page_size;
-        a.pages_per_seq = pages_per_seq;
-        a.max_seq_len = max_seq_len;
-        if (launch_decode_tc(a, stream) != cudaSuccess) {
-            cudaGetLastError();
-            return ATTN_ERR_LAUNCH;
-        }
-    }
     PrefixMergeArgs m;
     m.plan = pl;
     m.B = B;
     m.Hq = Hq;
+    m.Hkv = Hkv;
     const long long cap = static_cast<long long>(prefix_pages) * page_size;
     m.cap = static_cast<int>(cap < max_prefix_len ? cap : max_prefix_len);
     m.prefix_len = prefix_len;
@@ -922,6 +922,10 @@ extern "C" int attn_decode_prefix(const void *q, const void *k_pages, const void
     m.part_lse = pa.part_lse;
     m.o_suffix = own ? reinterpret_cast<float *>(at(sp.o_suffix)) : nullptr;
     m.lse_suffix = own ? reinterpret_cast<float *>(at(sp.lse_suffix)) : nullptr;
+    m.suffix_ws = own ? reinterpret_cast<float *>(at(sp.suffix_ws)) : nullptr;
+    m.suffix = suffix;
+    m.seq_lens = seq_lens;
+    m.suffix_cap = static_cast<int>(own_cap < max_seq_len ? own_cap : max_seq_len);
     m.o = o;
     m.lse = lse;
     if (launch_prefix_merge(m, stream) != cudaSuccess) {

@@ -159,8 +159,9 @@ struct TcParams {
     // e4m3 cache: the bf16 queries, read by the producer, and the per-(kv head, channel) coefficients
     const __nv_bfloat16 *q;
     const float *k_scale, *v_scale;
-    // kPart: the result stays in fp32 for a merge with attention over other keys; o is then unused
-    // and lse receives log2 units.
+    // kPart: the result stays in fp32 for a merge with attention over other keys. Whole pairs go to
+    // o_part [B][Hq][kD] and lse (log2 units), pieces of shared pairs stay in ws: the merge joins them.
+    // A pair may then hold fewer heads than G (the group's last, or a group that is no power of two).
     float *o_part;
 };
 
@@ -284,6 +285,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lane = threadIdx.x & 31;
     const int cta = blockIdx.x;
     const int pairs_per_b = p.Hkv * p.head_groups;
+    if constexpr (kPart)
+        asm volatile("griddepcontrol.launch_dependents;");  // the prefix's kernel needs nothing of this one
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -692,17 +695,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tS = tmem + lane_base;
         const uint32_t tO = tmem + lane_base + kColO;
         constexpr int n_out = G * kD;
-        if constexpr (kPaged) {
+        if constexpr (kPaged && !kPart) {
             // A sequence with no keys has nothing to attend to: O = 0 and LSE = -inf, written by
             // CTA (b mod P) since no unit of work names it.
             for (int b = cta; b < p.B; b += p.ctas) {
                 if (batch_len[b] != 0)
                     continue;
                 for (int h = 0; h < p.Hq; ++h) {
-                    if constexpr (kPart)
-                        p.o_part[(static_cast<size_t>(b) * p.Hq + h) * kD + i] = 0.f;
-                    else
-                        p.o[b * p.o_sb + h * p.o_sh + i] = __float2bfloat16_rn(0.f);
+                    p.o[b * p.o_sb + h * p.o_sh + i] = __float2bfloat16_rn(0.f);
                     if (i == 0)
                         p.lse[static_cast<size_t>(b) * p.Hq + h] = -INFINITY;
                 }
@@ -720,6 +720,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int bk = static_cast<int>(pair / p.head_groups);
             const int b = bk / p.Hkv;
             const int h0 = (bk % p.Hkv) * p.group + static_cast<int>(pair % p.head_groups) * G;
+            // kPart: heads of the pair; the columns behind them hold other heads' scores, taken as 0.
+            const int heads = kPart ? min(G, p.group - static_cast<int>(pair % p.head_groups) * G) : G;
             const int seq_len = kPaged ? batch_len[b] : p.Skv;
 
             // Factor from a score to log2 units, per head: the softmax scale times log2(e), and with
@@ -784,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const bool valid = (local0 + jr * kRound + sl) * kCK + i < seq_len;
 #pragma unroll
                             for (int h = 0; h < G; ++h)
-                                x[sl][h] = valid ? __uint_as_float(r[h]) * sl2[h] : -INFINITY;
+                                x[sl][h] = !valid ? -INFINITY : (kPart && h >= heads) ? 0.f : __uint_as_float(r[h]) * sl2[h];
                         }
                     }
                 }
@@ -979,6 +981,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     L += red_sum[(w * kN + h) * 2];
                     LPV += red_sum[(w * kN + h) * 2 + 1];
                 }
+                if (kPart && h >= heads)
+                    continue;
                 const float o = __uint_as_float(ov[h]) / LPV * v_coef;
                 const size_t bh = static_cast<size_t>(b) * p.Hq + h0 + h;
                 if (whole_pair) {
@@ -994,7 +998,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         slot_base[n_out + h] = m[h] + log2f(L);
                 }
             }
-            if (!whole_pair) {
+            if (!kPart && !whole_pair) {
                 // Signalled once the whole range is streamed (below): only the first and the last
                 // segment of a range can be a piece of a shared pair.
                 if (i == 0)
@@ -1005,7 +1009,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 
         // ---------------------------------------------------------------- shared pairs: the last CTA merges
-        if (ok) {
+        if (!kPart && ok) {
             int n_def = 0;
             if (i == 0) {
                 n_def = n_deferred;
@@ -1069,12 +1073,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         O = fmaf(w, __ldcg(sb + idx), O);
                     }
                     const size_t bh = static_cast<size_t>(b) * p.Hq + h0 + h;
-                    if constexpr (kPart)
-                        p.o_part[bh * kD + d] = O / W;
-                    else
-                        p.o[b * p.o_sb + (h0 + h) * p.o_sh + d] = __float2bfloat16_rn(O / W);
+                    p.o[b * p.o_sb + (h0 + h) * p.o_sh + d] = __float2bfloat16_rn(O / W);
                     if (d == 0)
-                        p.lse[bh] = (M + log2f(W)) * (kPart ? 1.f : kLn2);
+                        p.lse[bh] = (M + log2f(W)) * kLn2;
                 }
                 if (i == 0)
                     atomicExch(&p.counters[pr], 0);  // ready for the next call
@@ -1240,6 +1241,29 @@ cudaError_t decode_tc_ctas_per_sm(int G, bool fp8, int *ctas_per_sm)
 cudaError_t launch_decode_tc(const DecodeArgs &a, cudaStream_t stream) { return dispatch_tc(a.plan.G, &a, stream, nullptr); }
 
 size_t decode_tc_partial_floats(int G, int ctas) { return static_cast<size_t>(2) * ctas * (static_cast<size_t>(G) * kD + G); }
+
+cudaError_t decode_plan_suffix(int B, int Hq, int Hkv, int max_seq_len, int sm_count, DecodePlan *plan)
+{
+    DecodePlan pl;
+    const int group = Hq / Hkv;
+    // One pair holds the whole group up to the MMA's 16 columns, powers of two or not: the keys are
+    // then read once (a group of three as three pairs of one head took 2.9 times as long).
+    pl.G = 1;
+    while (pl.G < kN && pl.G < group)
+        pl.G *= 2;
+    pl.head_groups = (group + pl.G - 1) / pl.G;
+    pl.pairs = static_cast<long long>(B) * Hkv * pl.head_groups;
+    pl.ck = kCK;
+    pl.cpp = (max_seq_len + kCK - 1) / kCK;
+    pl.total = 0;
+    // One CTA per SM, or per chunk there can be: the others' SMs are then free for the prefix.
+    const long long most = pl.pairs * pl.cpp;
+    pl.ctas = static_cast<int>(most < 1 ? 1 : most < sm_count ? most : sm_count);
+    pl.max_contrib = 0;
+    pl.partial_floats = decode_tc_partial_floats(pl.G, pl.ctas);
+    *plan = pl;
+    return cudaSuccess;
+}
 
 cudaError_t decode_plan_paged(int B, int Hq, int Hkv, int max_seq_len, int requested_ctas, int sm_count,
                               DecodePlan *plan, bool fp8)

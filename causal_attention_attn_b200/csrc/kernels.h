@@ -11,6 +11,26 @@ namespace attn_b200 {
 // Devices the library keeps state for (function attributes, occupancy, workspaces), by index.
 constexpr int kMaxDevices = 64;
 
+// Launches `kernel`; with `overlap`, programmatically behind the kernel before it on the stream: it may
+// start once that one's blocks all run (or have called griddepcontrol.launch_dependents), and what it
+// needs of it lies behind its own griddepcontrol.wait.
+template <typename... Params, typename... Args>
+cudaError_t launch_behind(void (*kernel)(Params...), int grid, int threads, size_t smem, cudaStream_t stream, bool overlap,
+                          const Args &...args)
+{
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = overlap ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Index of the current device, or -1 if it cannot be read or is kMaxDevices or beyond. Function
 // attributes such as the dynamic shared-memory limit take effect on the device that is current
 // when they are set, so the launchers keep them per device.
@@ -148,19 +168,23 @@ struct PrefixArgs {
     float scale;
     PrefixPlan plan;
     float *part_o, *part_lse;
-    int *counters;  // n_counters ints, set to 0
-    int n_counters;
     int *status;
+    bool behind_suffix;  // launched right behind the suffixes' kernel: may overlap it
 };
 cudaError_t launch_prefix(const PrefixArgs &a, cudaStream_t stream, int *encode_error);
 
-// Joins the segments' partials and the suffixes' result (o_suffix fp32 [B][Hq][128], lse_suffix log2
-// units; null: no suffixes) into o (bf16) and lse (natural log).
+// Joins the segments' partials and the suffixes' result into o (bf16) and lse (natural log). The
+// suffixes' whole pairs are in o_suffix (fp32 [B][Hq][128]) and lse_suffix (log2 units), the pieces of
+// shared pairs in suffix_ws, as launch_decode left them.
 struct PrefixMergeArgs {
     PrefixPlan plan;
-    int B, Hq, cap;
+    int B, Hq, Hkv, cap;
     const int *prefix_len;
-    const float *part_o, *part_lse, *o_suffix, *lse_suffix;
+    const float *part_o, *part_lse;
+    const float *o_suffix, *lse_suffix, *suffix_ws;  // null: no suffixes
+    DecodePlan suffix;
+    const int *seq_lens;
+    int suffix_cap;
     void *o;
     float *lse;
 };
@@ -242,6 +266,9 @@ constexpr int kPagedMaxBatch = 1024;  // batch entries a paged decode may have (
 // upper bounds (cpp from max_seq_len; total is computed by each CTA); every pair may be shared.
 cudaError_t decode_plan_paged(int B, int Hq, int Hkv, int max_seq_len, int requested_ctas, int sm_count,
                               DecodePlan *plan, bool fp8 = false);
+// Plan of the suffixes of a shared-prefix decode: pairs hold up to 16 heads of a group of any size, and
+// the pieces of shared pairs are left in the workspace (launched with o_part given).
+cudaError_t decode_plan_suffix(int B, int Hq, int Hkv, int max_seq_len, int sm_count, DecodePlan *plan);
 cudaError_t launch_decode_tc(const DecodeArgs &a, cudaStream_t stream);
 
 // The status word of attn_decode_noalloc's fixed scratch array on the current device, or nullptr

@@ -98,81 +98,143 @@ cudaError_t launch_lse_merge(float *o_acc, float *lse_acc, const void *o_part, c
 
 namespace {
 
-// Attention of one row of a shared-prefix decode from its parts: the segments of its list of prefix
-// tiles (prefill_sm100.cu, decode_segment) and its own suffix, all fp32 with LSEs in log2 units:
+// Attention of one row of a shared-prefix decode from its parts, all fp32 with LSEs in log2 units: the
+// segments of its list of prefix tiles (prefill_sm100.cu, decode_segment) and its suffix, whole or in
+// the pieces that the CTAs which shared its pair left (decode_tc_sm100.cu).
 //   M = max LSE_s,  O = sum 2^(LSE_s - M) O_s / W,  lse = (M + log2 W) ln 2,  W = sum 2^(LSE_s - M).
-// One warp per row; the lanes look up the LSEs of 32 parts at a time, then each lane adds its four
-// channels over the parts. Bound by reading the parts, which the kernels before left in L2; every part
-// is read once. A row with no part (no prefix, no suffix) gives O = 0 and lse = -inf.
-__global__ void __launch_bounds__(256) prefix_merge_kernel(const PrefixMergeArgs a)
+// One warp per row: lane k looks up where part k lies and its LSE (both before any O is read), then
+// every lane adds its four channels over the parts, eight reads in flight. Bound by the latency of that
+// chain for few rows, by reading the parts (still in L2) for many. Where the parts lie follows from the
+// lengths alone and is computed before the wait for the kernels that write them. A row with no part (no
+// prefix, no suffix) gives O = 0 and lse = -inf.
+constexpr int kMergeWarps = 4;
+
+__global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const PrefixMergeArgs a)
 {
     constexpr int kTile = 128, D = 128;
     const int lane = threadIdx.x & 31;
-    const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    if (row >= static_cast<long long>(a.B) * a.Hq)
+    const int row = blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+    if (row >= a.B * a.Hq)
         return;
-    const int b = static_cast<int>(row / a.Hq), h = static_cast<int>(row % a.Hq);
+    const int b = row / a.Hq, h = row - b * a.Hq;
+
+    // Prefix: the CTAs from the one that holds the list's first unit to the one that holds its last; with
+    // fewer units than CTAs those between may hold none.
     const int tile = b / a.plan.tile_seqs;
     const int in_tile = (b - tile * a.plan.tile_seqs) * a.plan.group + h % a.plan.group;
     const long long list = static_cast<long long>(h / a.plan.group) * a.plan.tile_pairs + tile / 2;
-    const int len = min(max(__ldg(a.prefix_len), 0), a.cap);
-    const int tiles = (len + kTile - 1) / kTile;
+    const int tiles = (min(max(__ldg(a.prefix_len), 0), a.cap) + kTile - 1) / kTile;
     const long long total = a.plan.lists * tiles;
-    const int ctas = a.plan.ctas;
-    // The CTAs from the one that holds the list's first unit to the one that holds its last; with fewer
-    // units than CTAs those between may hold none.
-    int c0 = 0, n = 0;
+    int c0 = 0, n_prefix = 0;
     if (tiles > 0) {
-        c0 = static_cast<int>(((list * tiles + 1) * ctas - 1) / total);
-        n = static_cast<int>((((list + 1) * tiles) * ctas - 1) / total) - c0 + 1;
+        c0 = static_cast<int>(((list * tiles + 1) * a.plan.ctas - 1) / total);
+        n_prefix = static_cast<int>((((list + 1) * tiles) * a.plan.ctas - 1) / total) - c0 + 1;
     }
-    auto part_row = [&](int c) { return ((list + c) * 2 + (tile & 1)) * kTile + in_tile; };
-    auto lse_of = [&](int k) {
-        const int c = c0 + k;
-        if (k >= n || total * c / ctas >= total * (c + 1) / ctas)
-            return -INFINITY;
-        return __ldg(a.part_lse + part_row(c));
-    };
-    const float suffix = a.o_suffix ? __ldg(a.lse_suffix + row) : -INFINITY;
-    float M = suffix;
-    for (int k = 0; k < n; k += 32)
-        M = fmaxf(M, lse_of(k + lane));
+    // Suffix: its pair's units among all pairs' chunks laid end to end, as decode_tc_kernel lays them.
+    int s0 = 0, n_suffix = 0, in_pair = 0;
+    long long s_total = 0, s_first = 0;
+    bool whole = false;
+    if (a.o_suffix) {
+        const int group = a.Hq / a.Hkv, G = a.suffix.G, per_b = a.Hkv * a.suffix.head_groups;
+        long long before = 0, all = 0;
+        for (int i = lane; i < a.B; i += 32) {
+            const int chunks = (min(max(__ldg(a.seq_lens + i), 0), a.suffix_cap) + kTile - 1) / kTile;
+            all += chunks;
+            before += i < b ? chunks : 0;
+        }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float W = 0.f;
-    // A NaN LSE (from NaN scores) must not look like an empty part: M drops NaN, so weigh by the part.
-    auto weight = [&](float l) { return l == -INFINITY ? 0.f : exp2f(l - M); };
-    if (suffix != -INFINITY) {
-        const float w = weight(suffix);
-        const float4 v = __ldg(reinterpret_cast<const float4 *>(a.o_suffix + row * D) + lane);
-        acc = make_float4(w * v.x, w * v.y, w * v.z, w * v.w);
-        W = w;
+        for (int o = 16; o > 0; o >>= 1) {
+            all += __shfl_xor_sync(0xffffffffu, all, o);
+            before += __shfl_xor_sync(0xffffffffu, before, o);
+        }
+        const int chunks = (min(max(__ldg(a.seq_lens + b), 0), a.suffix_cap) + kTile - 1) / kTile;
+        const int g = h / group, in_group = h - g * group;
+        in_pair = in_group % G;
+        s_total = all * per_b;
+        s_first = before * per_b + static_cast<long long>(g * a.suffix.head_groups + in_group / G) * chunks;
+        if (chunks > 0) {
+            s0 = static_cast<int>(((s_first + 1) * a.suffix.ctas - 1) / s_total);
+            n_suffix = static_cast<int>(((s_first + chunks) * a.suffix.ctas - 1) / s_total) - s0 + 1;
+            whole = n_suffix == 1;
+        }
     }
+    const int n = n_prefix + n_suffix;
+    const size_t stride = static_cast<size_t>(a.suffix.G) * (D + 1);  // one piece in suffix_ws
+
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    // Part k: its O row and its LSE; -inf where there is none.
+    auto part = [&](int k, const float **o) -> float {
+        *o = a.part_o;
+        if (k < n_prefix) {
+            const int c = c0 + k;
+            if (total < a.plan.ctas && total * c / a.plan.ctas >= total * (c + 1) / a.plan.ctas)
+                return -INFINITY;
+            const long long r = ((list + c) * 2 + (tile & 1)) * kTile + in_tile;
+            *o = a.part_o + r * D;
+            return __ldcg(a.part_lse + r);
+        }
+        if (k >= n)
+            return -INFINITY;
+        if (whole) {
+            *o = a.o_suffix + static_cast<size_t>(row) * D;
+            return __ldcg(a.lse_suffix + row);
+        }
+        const int c = s0 + k - n_prefix;
+        const long long begin = s_total * c / a.suffix.ctas;
+        if (begin >= s_total * (c + 1) / a.suffix.ctas)
+            return -INFINITY;
+        const float *piece = a.suffix_ws + (static_cast<size_t>(c) * 2 + (begin >= s_first ? 0 : 1)) * stride;
+        *o = piece + in_pair * D;
+        return __ldcg(piece + a.suffix.G * D + in_pair);
+    };
+    float M = -INFINITY, W = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k = 0; k < n; k += 32) {
-        const float l = lse_of(k + lane);
-        const unsigned some = __ballot_sync(0xffffffffu, l != -INFINITY);
-        const float w = weight(l);
-#pragma unroll 4
-        for (int t = 0; t < min(32, n - k); ++t) {
-            const float wt = __shfl_sync(0xffffffffu, w, t);
-            if (!((some >> t) & 1u))
-                continue;
-            const float4 v = __ldg(reinterpret_cast<const float4 *>(a.part_o + part_row(c0 + k + t) * D) + lane);
-            acc.x = fmaf(wt, v.x, acc.x);
-            acc.y = fmaf(wt, v.y, acc.y);
-            acc.z = fmaf(wt, v.z, acc.z);
-            acc.w = fmaf(wt, v.w, acc.w);
-            W += wt;
+        const float *o;
+        const float l = part(k + lane, &o);
+        float m = l;
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1)
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+        const float new_m = fmaxf(M, m);
+        const float keep = M == -INFINITY ? 0.f : exp2f(M - new_m);
+        acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
+        W *= keep;
+        M = new_m;
+        // fmaxf drops NaN: a part with a NaN LSE (from NaN scores) keeps a NaN weight.
+        const float w = l == -INFINITY ? 0.f : exp2f(l - M);
+        const int parts = min(32, n - k);
+        for (int t = 0; t < parts; t += 8) {
+            float4 v[8];
+            float wt[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int from = min(t + j, 31);
+                wt[j] = __shfl_sync(0xffffffffu, w, from);
+                const float *po = reinterpret_cast<const float *>(
+                    __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), from));
+                // Behind the last part the weight is 0; an absent part's row is not read (it may hold NaN).
+                v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (t + j < parts && wt[j] != 0.f)
+                    v[j] = __ldcg(reinterpret_cast<const float4 *>(po) + lane);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                acc.x = fmaf(wt[j], v[j].x, acc.x);
+                acc.y = fmaf(wt[j], v[j].y, acc.y);
+                acc.z = fmaf(wt[j], v[j].z, acc.z);
+                acc.w = fmaf(wt[j], v[j].w, acc.w);
+                W += t + j < parts ? wt[j] : 0.f;
+            }
         }
     }
     const float inv = W == 0.f ? 0.f : 1.f / W;  // 0 only for a row without parts
-    __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
     uint2 out;
-    out.x = *reinterpret_cast<uint32_t *>(&lo);
-    out.y = *reinterpret_cast<uint32_t *>(&hi);
-    reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.o) + row * D)[lane] = out;
+    out.x = *reinterpret_cast<const uint32_t *>(&lo);
+    out.y = *reinterpret_cast<const uint32_t *>(&hi);
+    reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.o) + static_cast<size_t>(row) * D)[lane] = out;
     if (lane == 0)
         a.lse[row] = W == 0.f ? -INFINITY : (M + log2f(W)) * 0.6931471805599453f;
 }
@@ -181,9 +243,8 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const PrefixMergeArgs
 
 cudaError_t launch_prefix_merge(const PrefixMergeArgs &a, cudaStream_t stream)
 {
-    const long long rows = static_cast<long long>(a.B) * a.Hq;
-    prefix_merge_kernel<<<static_cast<unsigned>((rows + 7) / 8), 256, 0, stream>>>(a);
-    return cudaGetLastError();
+    const int rows = a.B * a.Hq;
+    return launch_behind(prefix_merge_kernel, (rows + kMergeWarps - 1) / kMergeWarps, 32 * kMergeWarps, 0, stream, true, a);
 }
 
 }  // namespace attn_b200

@@ -148,8 +148,6 @@ struct Params {
     int tile_seqs = 0;  // sequences in a 128-row tile
     int tile_pairs = 0; // pairs of tiles per head: heads * tile_pairs lists of KV tiles
     float *part_lse = nullptr;  // [segment slot][256], log2 units
-    int *counters = nullptr;    // the suffix kernel's arrival counters, cleared here
-    int n_counters = 0;
 };
 
 // What an instantiation of the kernel computes: attention over a dense cache, over a paged,
@@ -436,8 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint4 *>(smem + C::kOffQ + c * C::kChunkBytes + row * 128 + u * 16) = make_uint4(0u, 0u, 0u, 0u);
         }
         fence_proxy_async_smem();
-        for (int i = blockIdx.x * kThreads + threadIdx.x; i < p.n_counters; i += gridDim.x * kThreads)
-            p.counters[i] = 0;
+        asm volatile("griddepcontrol.launch_dependents;");  // the merge, which waits for this grid's end
     }
     if (warp == kWarpTma && lane == 0) {
         tma_prefetch_desc(&tm_q);
@@ -1040,6 +1037,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
 
+    // Shared prefix: this grid may have started while the suffixes' kernel ran; the merge behind this one
+    // waits for this grid only, so this grid ends after that one.
+    if (kMode == kPrefix && threadIdx.x == 0)
+        asm volatile("griddepcontrol.wait;" ::: "memory");
     tc_fence_before_sync();
     __syncthreads();
     if (warp == kWarpMma) {
@@ -1267,10 +1268,7 @@ cudaError_t launch_prefix(const PrefixArgs &a, cudaStream_t stream, int *encode_
     const long long cap = static_cast<long long>(a.prefix_pages) * a.page_size;
     p.cap = static_cast<int>(cap < a.max_prefix_len ? cap : a.max_prefix_len);
     p.part_lse = a.part_lse;
-    p.counters = a.counters;
-    p.n_counters = a.n_counters;
-    prefill_kernel<D, kPrefix><<<static_cast<unsigned>(pl.ctas), kThreads, C::kSmem, stream>>>(tq, tk, tv, to, p);
-    return cudaGetLastError();
+    return launch_behind(prefill_kernel<D, kPrefix>, pl.ctas, kThreads, C::kSmem, stream, a.behind_suffix, tq, tk, tv, to, p);
 }
 
 }  // namespace attn_b200
