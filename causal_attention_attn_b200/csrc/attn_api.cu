@@ -5,6 +5,7 @@
  */
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -844,6 +845,11 @@ extern "C" int attn_decode_prefix(const void *q, const void *k_pages, const void
         return rc;
     if (workspace_bytes < static_cast<long long>(sp.bytes))
         return ATTN_ERR_WORKSPACE;
+    // The prefix's units (KV tiles of all lists) are numbered in 31 bits.
+    const long long prefix_cap = std::min(static_cast<long long>(prefix_pages) * page_size,
+                                          static_cast<long long>(max_prefix_len));
+    if (pl.lists > INT_MAX / ((prefix_cap + 127) / 128 + 1))
+        return ATTN_ERR_SHAPE;
     if (!s->prefix_status) {
         void *word = nullptr;
         if (cudaGetSymbolAddress(&word, g_prefix_status) != cudaSuccess || !word) {
@@ -915,8 +921,7 @@ extern "C" int attn_decode_prefix(const void *q, const void *k_pages, const void
     m.B = B;
     m.Hq = Hq;
     m.Hkv = Hkv;
-    const long long cap = static_cast<long long>(prefix_pages) * page_size;
-    m.cap = static_cast<int>(cap < max_prefix_len ? cap : max_prefix_len);
+    m.cap = static_cast<int>(prefix_cap);
     m.prefix_len = prefix_len;
     m.part_o = pa.part_o;
     m.part_lse = pa.part_lse;

@@ -31,6 +31,20 @@ cudaError_t launch_behind(void (*kernel)(Params...), int grid, int threads, size
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// `total` units laid end to end, cut into `parts` ranges whose lengths differ by one at most (the first
+// total % parts are the longer ones): with fewer units than parts the last ranges are empty.
+struct EvenRange {
+    unsigned base, rem;
+    __host__ __device__ EvenRange(unsigned total, unsigned parts) : base(total / parts), rem(total % parts) {}
+    __host__ __device__ unsigned begin(unsigned c) const { return c * base + (c < rem ? c : rem); }
+    // The range that holds unit g < total.
+    __host__ __device__ unsigned part_of(unsigned g) const
+    {
+        const unsigned longer = rem * (base + 1);
+        return g < longer ? g / (base + 1) : rem + (g - longer) / base;
+    }
+};
+
 // Index of the current device, or -1 if it cannot be read or is kMaxDevices or beyond. Function
 // attributes such as the dynamic shared-memory limit take effect on the device that is current
 // when they are set, so the launchers keep them per device.

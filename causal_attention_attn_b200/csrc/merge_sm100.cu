@@ -118,17 +118,16 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const Pr
         return;
     const int b = row / a.Hq, h = row - b * a.Hq;
 
-    // Prefix: the CTAs from the one that holds the list's first unit to the one that holds its last; with
-    // fewer units than CTAs those between may hold none.
+    // Prefix: the CTAs from the one that holds the list's first unit to the one that holds its last.
     const int tile = b / a.plan.tile_seqs;
     const int in_tile = (b - tile * a.plan.tile_seqs) * a.plan.group + h % a.plan.group;
-    const long long list = static_cast<long long>(h / a.plan.group) * a.plan.tile_pairs + tile / 2;
+    const int list = h / a.plan.group * a.plan.tile_pairs + tile / 2;
     const int tiles = (min(max(__ldg(a.prefix_len), 0), a.cap) + kTile - 1) / kTile;
-    const long long total = a.plan.lists * tiles;
     int c0 = 0, n_prefix = 0;
     if (tiles > 0) {
-        c0 = static_cast<int>(((list * tiles + 1) * a.plan.ctas - 1) / total);
-        n_prefix = static_cast<int>((((list + 1) * tiles) * a.plan.ctas - 1) / total) - c0 + 1;
+        const EvenRange range(static_cast<unsigned>(a.plan.lists) * tiles, a.plan.ctas);
+        c0 = static_cast<int>(range.part_of(list * tiles));
+        n_prefix = static_cast<int>(range.part_of((list + 1) * tiles - 1)) - c0 + 1;
     }
     // Suffix: its pair's units among all pairs' chunks laid end to end, as decode_tc_kernel lays them.
     int s0 = 0, n_suffix = 0, in_pair = 0;
@@ -168,9 +167,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const Pr
         *o = a.part_o;
         if (k < n_prefix) {
             const int c = c0 + k;
-            if (total < a.plan.ctas && total * c / a.plan.ctas >= total * (c + 1) / a.plan.ctas)
-                return -INFINITY;
-            const long long r = ((list + c) * 2 + (tile & 1)) * kTile + in_tile;
+            const long long r = (static_cast<long long>(list + c) * 2 + (tile & 1)) * kTile + in_tile;
             *o = a.part_o + r * D;
             return __ldcg(a.part_lse + r);
         }

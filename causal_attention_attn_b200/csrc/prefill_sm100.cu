@@ -147,6 +147,7 @@ struct Params {
     int sub_groups = 1; // equal parts of a kv head's group of more than 128 query heads; group is one part
     int tile_seqs = 0;  // sequences in a 128-row tile
     int tile_pairs = 0; // pairs of tiles per head: heads * tile_pairs lists of KV tiles
+    float *part_o = nullptr;    // [segment slot][256][128]
     float *part_lse = nullptr;  // [segment slot][256], log2 units
 };
 
@@ -253,43 +254,53 @@ struct Item {
 
 // ---- shared prefix of a decode ------------------------------------------------------------------
 // For each head and pair of tiles there is a list of all KV tiles of the prefix; the lists, laid end
-// to end, are cut into one range per CTA of equal length, so that a few rows still use every SM. A
-// CTA's part of one list is a segment: an item whose unnormalised softmax is finished here and
-// whose rows are merged with the list's other segments, and with the sequences' own keys, by
-// prefix_merge_kernel. Segment (list, CTA) has slot list + CTA: both grow along the lists, and one of
-// them does from each segment to the next, so slots are distinct and below lists + CTAs.
+// to end, are cut into one range per CTA (even_range: lengths differ by one at most), so that a few rows
+// still use every SM. A CTA's part of one list is a segment: an item whose unnormalised softmax is
+// finished here and whose rows are merged with the list's other segments, and with the sequences' own
+// keys, by prefix_merge_kernel. Segment (list, CTA) has slot list + CTA: both grow along the lists, and
+// one of them does from each segment to the next, so slots are distinct and below lists + CTAs.
 
 __device__ __forceinline__ int prefix_length(const Params &p) { return min(max(__ldg(p.seq_lens), 0), p.cap); }
 
-__device__ __forceinline__ long long segment_begin(long long total, int c, int ctas) { return total * c / ctas; }
+// Segments of this CTA, worked out once (s_segments): list and range of the r-th are plain arithmetic.
+struct Segments {
+    int len, tiles;       // the prefix's keys and KV tiles
+    int begin, end;       // this CTA's range
+    int first_list;       // list that holds `begin`
+};
+__shared__ Segments s_segments;
+
+__device__ __forceinline__ Segments find_segments(const Params &p)
+{
+    Segments sg;
+    sg.len = prefix_length(p);
+    sg.tiles = (sg.len + kBN - 1) / kBN;
+    const uint32_t total = static_cast<uint32_t>(p.heads) * p.tile_pairs * sg.tiles;
+    const EvenRange r(total, gridDim.x);
+    sg.begin = static_cast<int>(r.begin(blockIdx.x));
+    sg.end = static_cast<int>(r.begin(blockIdx.x + 1));
+    sg.first_list = sg.tiles ? sg.begin / sg.tiles : 0;
+    return sg;
+}
 
 // List of this CTA's r-th segment, or -1.
-__device__ __forceinline__ int segment_index(const Params &p, int r)
+__device__ __forceinline__ int segment_index(int r)
 {
-    const int tiles = (prefix_length(p) + kBN - 1) / kBN;
-    const int lists = p.heads * p.tile_pairs;
-    const long long total = static_cast<long long>(lists) * tiles;
-    const int ctas = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
-    const long long g0 = segment_begin(total, c, ctas), g1 = segment_begin(total, c + 1, ctas);
-    if (g0 >= g1)
-        return -1;
-    const long long list = g0 / tiles + r;
-    return list * tiles < g1 ? static_cast<int>(list) : -1;
+    const Segments &sg = s_segments;
+    const int list = sg.first_list + r;
+    return sg.begin < sg.end && list * sg.tiles < sg.end ? list : -1;
 }
 
 __device__ __forceinline__ Item decode_segment(const Params &p, int list)
 {
+    const Segments &sg = s_segments;
     Item it;
-    it.skv = prefix_length(p);
+    it.skv = sg.len;
     it.off = 0;
     it.b = 0;
-    const int tiles = (it.skv + kBN - 1) / kBN;
-    const long long total = static_cast<long long>(p.heads) * p.tile_pairs * tiles;
-    const int ctas = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
-    const long long g0 = segment_begin(total, c, ctas), g1 = segment_begin(total, c + 1, ctas);
-    const long long first = static_cast<long long>(list) * tiles;
-    it.kt0 = static_cast<int>(max(g0 - first, 0LL));
-    const int n = static_cast<int>(min(g1 - first, static_cast<long long>(tiles))) - it.kt0;
+    const int first = list * sg.tiles;
+    it.kt0 = max(sg.begin - first, 0);
+    const int n = min(sg.end - first, sg.tiles) - it.kt0;
     it.kvh = list / p.tile_pairs;
     const int pair = list - it.kvh * p.tile_pairs;
     it.q0[0] = 2 * pair * p.tile_seqs;
@@ -297,7 +308,7 @@ __device__ __forceinline__ Item decode_segment(const Params &p, int list)
     it.hq[0] = it.hq[1] = it.kvh;
     it.n[0] = n;
     it.n[1] = it.q0[1] < p.B ? n : 0;
-    it.slot = list + c;
+    it.slot = list + static_cast<int>(blockIdx.x);
     return it;
 }
 
@@ -351,7 +362,7 @@ __device__ __forceinline__ Item decode_item(const Params &p, int w)
 template <int kMode>
 __device__ __forceinline__ int next_work(const Params &p, int r)
 {
-    return kMode == kPrefix ? segment_index(p, r) : work_index(p, r);
+    return kMode == kPrefix ? segment_index(r) : work_index(p, r);
 }
 
 // The first of this CTA's items from the r-th on that has a KV tile to stream, or -1. Without a
@@ -434,6 +445,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint4 *>(smem + C::kOffQ + c * C::kChunkBytes + row * 128 + u * 16) = make_uint4(0u, 0u, 0u, 0u);
         }
         fence_proxy_async_smem();
+        if (warp == 11 && lane == 0)
+            s_segments = find_segments(p);
         asm volatile("griddepcontrol.launch_dependents;");  // the merge, which waits for this grid's end
     }
     if (warp == kWarpTma && lane == 0) {
@@ -942,29 +955,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             // Paged: a row that saw no key has l = 0: O = 0 and LSE = m + log2(0) = -inf.
             const float inv_l = (kPaged && !(l_pv > 0.f)) ? 0.f : 1.f / l_pv;
             if constexpr (kMode == kPrefix) {
-                // Partials: normalised O in fp32, 32 dims at a time through the warp's staging box (as the
-                // bf16 O below), and the LSE in log2 units. Rows behind the last sequence are written too
-                // (the slot has room for every row) and never read.
-                const uint32_t wstage = s_base + C::kOffStage + static_cast<uint32_t>(warp) * C::kWarpStageBytes;
-                uint8_t *wrow = smem + C::kOffStage + warp * C::kWarpStageBytes + lane * 128;
+                // Partials: normalised O in fp32, 32 dims at a time turned in the warp's staging box (16-byte
+                // units XOR row % 8) so that eight lanes store one row's 128 bytes, and the LSE in log2
+                // units. (TMA stores from the box, waiting for each to be read, took 1.9 us a tile.)
+                // Rows behind the last sequence are written too (the slot has room) and never read.
+                float *box = reinterpret_cast<float *>(smem + C::kOffStage + warp * C::kWarpStageBytes);
                 const int row0 = (cur.slot * 2 + x) * kBM + 32 * (warp & 3);
-#pragma unroll 1
+                float *dst = p.part_o + static_cast<size_t>(row0) * D;
+                const int rr = lane >> 3, uu = lane & 7;
+#pragma unroll
                 for (int h = 0; h < D / 32; ++h) {
                     uint32_t ov[32];
                     tmem_ld32_wait(tO + h * 32, ov);
-                    if (lane == 0)
-                        bulk_wait_group_read0();
-                    __syncwarp();
+                    __syncwarp();  // the rows of the 32 dims before are read
 #pragma unroll
                     for (int u = 0; u < 8; ++u)
-                        *reinterpret_cast<float4 *>(wrow + ((u ^ (lane & 7)) << 4)) =
+                        *reinterpret_cast<float4 *>(box + lane * 32 + ((u ^ (lane & 7)) << 2)) =
                             make_float4(__uint_as_float(ov[4 * u]) * inv_l, __uint_as_float(ov[4 * u + 1]) * inv_l,
                                         __uint_as_float(ov[4 * u + 2]) * inv_l, __uint_as_float(ov[4 * u + 3]) * inv_l);
-                    fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0 && 32 * (warp & 3) < p.tile_seqs * p.group) {
-                        tma_store_4d(&tm_o, wstage, h * 32, row0, 0, 0);
-                        bulk_commit_group();
+#pragma unroll
+                    for (int t = 0; t < 8; ++t) {
+                        const int r4 = 4 * t + rr;
+                        const float4 v = *reinterpret_cast<const float4 *>(box + r4 * 32 + ((uu ^ (r4 & 7)) << 2));
+                        __stcg(reinterpret_cast<float4 *>(dst + static_cast<size_t>(r4) * D + h * 32) + uu, v);
                     }
                 }
                 p.part_lse[row0 + lane] = m + log2f(l);
@@ -1028,7 +1042,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 p.lse[bh_q * p.Sq + row] = (m + log2f(l)) * kLn2;
             tc_fence_before_sync();
         }
-        if constexpr (C::kTmaStore) {
+        if constexpr (C::kTmaStore && kMode != kPrefix) {
             // Every store issued by this warp has completed (its staging is read and O is written)
             // before the CTA can exit.
             if (lane == 0)
@@ -1048,20 +1062,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_dealloc(tmem, kTmemCols);
     }
 #undef BAR
-}
-
-// The partials of a shared prefix: fp32 [rows][128], stored in boxes of 32 dims x 32 rows.
-bool make_map_partials(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap *map, float *base, long long rows, int *err)
-{
-    const cuuint64_t dims[4] = {128, static_cast<cuuint64_t>(rows), 1, 1};
-    const cuuint64_t strides[3] = {512, static_cast<cuuint64_t>(rows) * 512, static_cast<cuuint64_t>(rows) * 512};
-    const cuuint32_t box[4] = {32, 32, 1, 1}, estr[4] = {1, 1, 1, 1};
-    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, base, dims, strides, box, estr,
-                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS)
-        *err = static_cast<int>(r);
-    return r == CUDA_SUCCESS;
 }
 
 // Sets an instantiation's attributes on the current device once.
@@ -1242,9 +1242,9 @@ cudaError_t launch_prefix(const PrefixArgs &a, cudaStream_t stream, int *encode_
     if (!make_map4(encode, &tk, a.k_pages, 2, D, a.page_size, a.Hkv, a.num_pages, pst, 64, rows, CU_TENSOR_MAP_SWIZZLE_128B,
                    encode_error) ||
         !make_map4(encode, &tv, a.v_pages, 2, D, a.page_size, a.Hkv, a.num_pages, pst, 64, rows, CU_TENSOR_MAP_SWIZZLE_128B,
-                   encode_error) ||
-        !make_map_partials(encode, &to, a.part_o, static_cast<long long>(pl.slots) * 2 * kBM, encode_error))
+                   encode_error))
         return cudaErrorInvalidValue;
+    to = tq;  // unused: the partials leave by plain stores
     const cudaError_t ready = prepare<D, kPrefix>();
     if (ready != cudaSuccess)
         return ready;
@@ -1267,6 +1267,7 @@ cudaError_t launch_prefix(const PrefixArgs &a, cudaStream_t stream, int *encode_
     p.pages_per_seq = a.prefix_pages;
     const long long cap = static_cast<long long>(a.prefix_pages) * a.page_size;
     p.cap = static_cast<int>(cap < a.max_prefix_len ? cap : a.max_prefix_len);
+    p.part_o = a.part_o;
     p.part_lse = a.part_lse;
     return launch_behind(prefill_kernel<D, kPrefix>, pl.ctas, kThreads, C::kSmem, stream, a.behind_suffix, tq, tk, tv, to, p);
 }
