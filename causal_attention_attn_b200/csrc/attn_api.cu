@@ -739,10 +739,10 @@ namespace {
 
 // attn_decode_prefix's workspace, cut up.
 struct PrefixSpace {
-    size_t suffix_ws, o_suffix, lse_suffix, part_o, part_lse, bytes;  // byte offsets
+    size_t pieces, o_suffix, lse_suffix, part_o, part_lse, bytes;  // byte offsets
 };
 
-PrefixSpace prefix_space(int B, int Hq, const PrefixPlan &pl, const DecodePlan &suffix)
+PrefixSpace prefix_space(int B, int Hq, const PrefixPlan &pl, const SuffixPlan &suffix)
 {
     size_t at = 0;
     auto take = [&](size_t n) {
@@ -752,7 +752,7 @@ PrefixSpace prefix_space(int B, int Hq, const PrefixPlan &pl, const DecodePlan &
     };
     PrefixSpace sp;
     const size_t rows = static_cast<size_t>(B) * Hq;
-    sp.suffix_ws = take(suffix.partial_floats * sizeof(float));
+    sp.pieces = take(suffix.piece_floats * sizeof(float));
     sp.o_suffix = take(rows * 128 * sizeof(float));
     sp.lse_suffix = take(rows * sizeof(float));
     sp.part_o = take(static_cast<size_t>(pl.slots) * 256 * 128 * sizeof(float));
@@ -775,11 +775,10 @@ int check_prefix_sizes(int B, int Hq, int Hkv, int max_prefix_len, int max_seq_l
 
 // Both plans and the workspace's parts on the current device (g_mutex held).
 int plan_prefix(const DeviceState &s, int B, int Hq, int Hkv, int max_prefix_len, int max_seq_len, PrefixPlan *pl,
-                DecodePlan *suffix, PrefixSpace *sp)
+                SuffixPlan *suffix, PrefixSpace *sp)
 {
     *pl = prefix_plan(B, Hq, Hkv, max_prefix_len, s.sm_count);
-    if (decode_plan_suffix(B, Hq, Hkv, max_seq_len, s.sm_count, suffix) != cudaSuccess)
-        return ATTN_ERR_SHAPE;
+    *suffix = suffix_plan(B, Hq, Hkv, max_seq_len, s.sm_count);
     if (pl->slots * 256 > INT_MAX)
         return ATTN_ERR_SHAPE;
     *sp = prefix_space(B, Hq, *pl, *suffix);
@@ -799,7 +798,7 @@ extern "C" long long attn_decode_prefix_workspace(int B, int Hq, int Hkv, int ma
     if (!s)
         return err;
     PrefixPlan pl;
-    DecodePlan suffix;
+    SuffixPlan suffix;
     PrefixSpace sp;
     rc = plan_prefix(*s, B, Hq, Hkv, max_prefix_len, max_seq_len, &pl, &suffix, &sp);
     return rc != ATTN_OK ? rc : static_cast<long long>(sp.bytes);
@@ -838,17 +837,19 @@ extern "C" int attn_decode_prefix(const void *q, const void *k_pages, const void
     if (!s)
         return err;
     PrefixPlan pl;
-    DecodePlan suffix;
+    SuffixPlan suffix;
     PrefixSpace sp;
     rc = plan_prefix(*s, B, Hq, Hkv, max_prefix_len, max_seq_len, &pl, &suffix, &sp);
     if (rc != ATTN_OK)
         return rc;
     if (workspace_bytes < static_cast<long long>(sp.bytes))
         return ATTN_ERR_WORKSPACE;
-    // The prefix's units (KV tiles of all lists) are numbered in 31 bits.
+    // The prefix's units (KV tiles of all lists) and the suffixes' are numbered in 31 bits.
     const long long prefix_cap = std::min(static_cast<long long>(prefix_pages) * page_size,
                                           static_cast<long long>(max_prefix_len));
-    if (pl.lists > INT_MAX / ((prefix_cap + 127) / 128 + 1))
+    const long long own_cap = std::min(static_cast<long long>(pages_per_seq) * page_size, static_cast<long long>(max_seq_len));
+    const long long own_pairs = static_cast<long long>(B) * Hkv * suffix.head_groups;
+    if (pl.lists > INT_MAX / ((prefix_cap + 127) / 128 + 1) || own_pairs > INT_MAX / (own_cap / kSuffixUnitKeys + 2))
         return ATTN_ERR_SHAPE;
     if (!s->prefix_status) {
         void *word = nullptr;
@@ -862,34 +863,30 @@ extern "C" int attn_decode_prefix(const void *q, const void *k_pages, const void
     // The suffixes first: the prefix's kernel needs nothing of theirs and starts on the SMs that they
     // leave free; the merge waits for both.
     const bool own = max_seq_len > 0;
-    const long long own_cap = static_cast<long long>(pages_per_seq) * page_size;
+    int encode_error = 0;
     if (own) {
-        DecodeArgs a;
+        SuffixArgs a;
         a.q = q;
-        a.k = k_pages;
-        a.v = v_pages;
-        a.o = nullptr;
-        a.o_part = reinterpret_cast<float *>(at(sp.o_suffix));
+        a.k_pages = k_pages;
+        a.v_pages = v_pages;
+        a.seq_lens = seq_lens;
+        a.block_table = block_table;
+        a.o = reinterpret_cast<float *>(at(sp.o_suffix));
         a.lse = reinterpret_cast<float *>(at(sp.lse_suffix));
+        a.pieces = reinterpret_cast<float *>(at(sp.pieces));
         a.B = B;
         a.Hq = Hq;
         a.Hkv = Hkv;
-        a.Skv = 0;
-        a.D = 128;
-        a.scale = scale;
-        a.plan = suffix;
-        a.ws = reinterpret_cast<float *>(at(sp.suffix_ws));
-        a.counters = nullptr;  // no pair is merged in the kernel
-        a.status = s->prefix_status;
-        a.seq_lens = seq_lens;
-        a.block_table = block_table;
         a.num_pages = num_pages;
         a.page_size = page_size;
         a.pages_per_seq = pages_per_seq;
-        a.max_seq_len = max_seq_len;
-        if (launch_decode_tc(a, stream) != cudaSuccess) {
+        a.cap = static_cast<int>(own_cap);
+        a.scale = scale;
+        a.plan = suffix;
+        a.status = s->prefix_status;
+        if (launch_suffix(a, stream, &encode_error) != cudaSuccess) {
             cudaGetLastError();
-            return ATTN_ERR_LAUNCH;
+            return encode_error ? ATTN_ERR_CUDA : ATTN_ERR_LAUNCH;
         }
     }
     PrefixArgs pa;
@@ -911,7 +908,6 @@ extern "C" int attn_decode_prefix(const void *q, const void *k_pages, const void
     pa.part_lse = reinterpret_cast<float *>(at(sp.part_lse));
     pa.status = s->prefix_status;
     pa.behind_suffix = own;
-    int encode_error = 0;
     if (launch_prefix(pa, stream, &encode_error) != cudaSuccess) {
         cudaGetLastError();
         return encode_error ? ATTN_ERR_CUDA : ATTN_ERR_LAUNCH;
@@ -927,10 +923,10 @@ extern "C" int attn_decode_prefix(const void *q, const void *k_pages, const void
     m.part_lse = pa.part_lse;
     m.o_suffix = own ? reinterpret_cast<float *>(at(sp.o_suffix)) : nullptr;
     m.lse_suffix = own ? reinterpret_cast<float *>(at(sp.lse_suffix)) : nullptr;
-    m.suffix_ws = own ? reinterpret_cast<float *>(at(sp.suffix_ws)) : nullptr;
+    m.pieces = own ? reinterpret_cast<float *>(at(sp.pieces)) : nullptr;
     m.suffix = suffix;
     m.seq_lens = seq_lens;
-    m.suffix_cap = static_cast<int>(own_cap < max_seq_len ? own_cap : max_seq_len);
+    m.suffix_cap = static_cast<int>(own_cap);
     m.o = o;
     m.lse = lse;
     if (launch_prefix_merge(m, stream) != cudaSuccess) {

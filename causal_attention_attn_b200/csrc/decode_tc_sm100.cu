@@ -159,10 +159,6 @@ struct TcParams {
     // e4m3 cache: the bf16 queries, read by the producer, and the per-(kv head, channel) coefficients
     const __nv_bfloat16 *q;
     const float *k_scale, *v_scale;
-    // kPart: the result stays in fp32 for a merge with attention over other keys. Whole pairs go to
-    // o_part [B][Hq][kD] and lse (log2 units), pieces of shared pairs stay in ws: the merge joins them.
-    // A pair may then hold fewer heads than G (the group's last, or a group that is no power of two).
-    float *o_part;
 };
 
 __device__ __forceinline__ float ex2(float x)
@@ -246,7 +242,7 @@ struct UnitPos {
     int local, cpp;
 };
 
-template <int G, bool kPaged, bool kFp8, bool kPart>
+template <int G, bool kPaged, bool kFp8>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const TcParams p)
@@ -285,8 +281,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lane = threadIdx.x & 31;
     const int cta = blockIdx.x;
     const int pairs_per_b = p.Hkv * p.head_groups;
-    if constexpr (kPart)
-        asm volatile("griddepcontrol.launch_dependents;");  // the prefix's kernel needs nothing of this one
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -695,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tS = tmem + lane_base;
         const uint32_t tO = tmem + lane_base + kColO;
         constexpr int n_out = G * kD;
-        if constexpr (kPaged && !kPart) {
+        if constexpr (kPaged) {
             // A sequence with no keys has nothing to attend to: O = 0 and LSE = -inf, written by
             // CTA (b mod P) since no unit of work names it.
             for (int b = cta; b < p.B; b += p.ctas) {
@@ -720,8 +714,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int bk = static_cast<int>(pair / p.head_groups);
             const int b = bk / p.Hkv;
             const int h0 = (bk % p.Hkv) * p.group + static_cast<int>(pair % p.head_groups) * G;
-            // kPart: heads of the pair; the columns behind them hold other heads' scores, taken as 0.
-            const int heads = kPart ? min(G, p.group - static_cast<int>(pair % p.head_groups) * G) : G;
             const int seq_len = kPaged ? batch_len[b] : p.Skv;
 
             // Factor from a score to log2 units, per head: the softmax scale times log2(e), and with
@@ -786,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const bool valid = (local0 + jr * kRound + sl) * kCK + i < seq_len;
 #pragma unroll
                             for (int h = 0; h < G; ++h)
-                                x[sl][h] = !valid ? -INFINITY : (kPart && h >= heads) ? 0.f : __uint_as_float(r[h]) * sl2[h];
+                                x[sl][h] = valid ? __uint_as_float(r[h]) * sl2[h] : -INFINITY;
                         }
                     }
                 }
@@ -981,24 +973,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     L += red_sum[(w * kN + h) * 2];
                     LPV += red_sum[(w * kN + h) * 2 + 1];
                 }
-                if (kPart && h >= heads)
-                    continue;
                 const float o = __uint_as_float(ov[h]) / LPV * v_coef;
                 const size_t bh = static_cast<size_t>(b) * p.Hq + h0 + h;
                 if (whole_pair) {
-                    if constexpr (kPart)
-                        p.o_part[bh * kD + i] = o;
-                    else
-                        p.o[b * p.o_sb + (h0 + h) * p.o_sh + i] = __float2bfloat16_rn(o);
+                    p.o[b * p.o_sb + (h0 + h) * p.o_sh + i] = __float2bfloat16_rn(o);
                     if (i == h)
-                        p.lse[bh] = (m[h] + log2f(L)) * (kPart ? 1.f : kLn2);
+                        p.lse[bh] = (m[h] + log2f(L)) * kLn2;
                 } else {
                     slot_base[h * kD + i] = o;
                     if (i == h)
                         slot_base[n_out + h] = m[h] + log2f(L);
                 }
             }
-            if (!kPart && !whole_pair) {
+            if (!whole_pair) {
                 // Signalled once the whole range is streamed (below): only the first and the last
                 // segment of a range can be a piece of a shared pair.
                 if (i == 0)
@@ -1009,7 +996,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 
         // ---------------------------------------------------------------- shared pairs: the last CTA merges
-        if (!kPart && ok) {
+        if (ok) {
             int n_def = 0;
             if (i == 0) {
                 n_def = n_deferred;
@@ -1092,7 +1079,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #undef BAR
 }
 
-template <int G, bool kPaged, bool kFp8, bool kPart = false>
+template <int G, bool kPaged, bool kFp8>
 cudaError_t prepare_g(int *ctas_per_sm)
 {
     static int cached_per_dev[kMaxDevices] = {};  // per device: attributes apply to the current one
@@ -1102,11 +1089,11 @@ cudaError_t prepare_g(int *ctas_per_sm)
         return cudaErrorInvalidDevice;
     int &cached = cached_per_dev[dev];
     if (cached == 0) {
-        cudaError_t e = cudaFuncSetAttribute(decode_tc_kernel<G, kPaged, kFp8, kPart>,
+        cudaError_t e = cudaFuncSetAttribute(decode_tc_kernel<G, kPaged, kFp8>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         int n = 0;
         if (e == cudaSuccess)
-            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_tc_kernel<G, kPaged, kFp8, kPart>, kThreads, kSmem);
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_tc_kernel<G, kPaged, kFp8>, kThreads, kSmem);
         if (e != cudaSuccess)
             return e;
         cached = n > 0 ? n : 1;
@@ -1116,10 +1103,10 @@ cudaError_t prepare_g(int *ctas_per_sm)
     return cudaSuccess;
 }
 
-template <int G, bool kPaged, bool kFp8, bool kPart = false>
+template <int G, bool kPaged, bool kFp8>
 cudaError_t launch_g(const DecodeArgs &a, cudaStream_t stream)
 {
-    cudaError_t e = prepare_g<G, kPaged, kFp8, kPart>(nullptr);
+    cudaError_t e = prepare_g<G, kPaged, kFp8>(nullptr);
     if (e != cudaSuccess)
         return e;
     auto encode = get_encode_fn();
@@ -1184,8 +1171,7 @@ cudaError_t launch_g(const DecodeArgs &a, cudaStream_t stream)
     p.q = static_cast<const __nv_bfloat16 *>(a.q);
     p.k_scale = a.k_scale;
     p.v_scale = a.v_scale;
-    p.o_part = a.o_part;
-    decode_tc_kernel<G, kPaged, kFp8, kPart>
+    decode_tc_kernel<G, kPaged, kFp8>
         <<<static_cast<unsigned>(pl.ctas), kThreads, Lay<kFp8>::kSmem, stream>>>(tq, tk, tv, p);
     return cudaGetLastError();
 }
@@ -1195,8 +1181,6 @@ cudaError_t dispatch_g(const DecodeArgs *a, cudaStream_t stream, int *ctas_per_s
 {
     if (!a)
         return fp8 ? prepare_g<G, false, true>(ctas_per_sm) : prepare_g<G, false, false>(ctas_per_sm);
-    if (a->o_part)  // the suffixes of a shared-prefix decode: paged, bf16
-        return launch_g<G, true, false, true>(*a, stream);
     if (a->fp8)
         return a->seq_lens ? launch_g<G, true, true>(*a, stream) : launch_g<G, false, true>(*a, stream);
     return a->seq_lens ? launch_g<G, true, false>(*a, stream) : launch_g<G, false, false>(*a, stream);
@@ -1241,29 +1225,6 @@ cudaError_t decode_tc_ctas_per_sm(int G, bool fp8, int *ctas_per_sm)
 cudaError_t launch_decode_tc(const DecodeArgs &a, cudaStream_t stream) { return dispatch_tc(a.plan.G, &a, stream, nullptr); }
 
 size_t decode_tc_partial_floats(int G, int ctas) { return static_cast<size_t>(2) * ctas * (static_cast<size_t>(G) * kD + G); }
-
-cudaError_t decode_plan_suffix(int B, int Hq, int Hkv, int max_seq_len, int sm_count, DecodePlan *plan)
-{
-    DecodePlan pl;
-    const int group = Hq / Hkv;
-    // One pair holds the whole group up to the MMA's 16 columns, powers of two or not: the keys are
-    // then read once (a group of three as three pairs of one head took 2.9 times as long).
-    pl.G = 1;
-    while (pl.G < kN && pl.G < group)
-        pl.G *= 2;
-    pl.head_groups = (group + pl.G - 1) / pl.G;
-    pl.pairs = static_cast<long long>(B) * Hkv * pl.head_groups;
-    pl.ck = kCK;
-    pl.cpp = (max_seq_len + kCK - 1) / kCK;
-    pl.total = 0;
-    // One CTA per SM, or per chunk there can be: the others' SMs are then free for the prefix.
-    const long long most = pl.pairs * pl.cpp;
-    pl.ctas = static_cast<int>(most < 1 ? 1 : most < sm_count ? most : sm_count);
-    pl.max_contrib = 0;
-    pl.partial_floats = decode_tc_partial_floats(pl.G, pl.ctas);
-    *plan = pl;
-    return cudaSuccess;
-}
 
 cudaError_t decode_plan_paged(int B, int Hq, int Hkv, int max_seq_len, int requested_ctas, int sm_count,
                               DecodePlan *plan, bool fp8)

@@ -74,6 +74,7 @@ enum WaitSite : int {
     kSiteDecodeConsumer = 17,
     kSiteBwd = 24,
     kSiteFp8Prefill = 32,
+    kSiteSuffix = 40,
 };
 
 // Element strides of a [batch][head][row][dim] tensor with a contiguous dim (see tma_host.h).
@@ -138,9 +139,6 @@ struct DecodeArgs {
     // [Hkv][D] coefficients (value = code * coefficient of its kv head and channel).
     bool fp8 = false;
     const float *k_scale = nullptr, *v_scale = nullptr;
-    // Paged bf16 cache of the tensor-core decode only: when given, O goes here in fp32 [B][Hq][D] (o is
-    // not written) and lse in log2 units, for a merge with attention over other keys.
-    float *o_part = nullptr;
 };
 
 // ATTN_OK with the current device's SM count, or the attn_status that says why it cannot be used.
@@ -187,16 +185,48 @@ struct PrefixArgs {
 };
 cudaError_t launch_prefix(const PrefixArgs &a, cudaStream_t stream, int *encode_error);
 
-// Joins the segments' partials and the suffixes' result into o (bf16) and lse (natural log). The
-// suffixes' whole pairs are in o_suffix (fp32 [B][Hq][128]) and lse_suffix (log2 units), the pieces of
-// shared pairs in suffix_ws, as launch_decode left them.
+// The suffixes of a shared-prefix decode (head dim 128, paged bf16 cache): each sequence's token over its
+// own keys. A pair is one (sequence, kv head, up to 16 query heads), its keys are units of 16; all pairs'
+// units, sequence by sequence, are cut evenly over the workers (warps). Whole pairs leave their result
+// in o (fp32 [B][Hq][128], normalised) and lse (log2 units); a worker's first and last piece of a shared
+// pair are at pieces + (2 worker + (0 or 1)) * suffix_piece(heads_per_pair): O rows, then LSEs.
+constexpr int kSuffixWarps = 12;      // workers of a CTA
+constexpr int kSuffixUnitKeys = 16;
+constexpr int kSuffixMinUnits = 2;    // units a worker has at least, while there are fewer than workers
+// Workers that share `total` units in a grid of `ctas`.
+__host__ __device__ inline int suffix_workers(int total, int ctas)
+{
+    const int want = (total + kSuffixMinUnits - 1) / kSuffixMinUnits, most = ctas * kSuffixWarps;
+    return want < most ? want : most;
+}
+// Floats of one piece; a multiple of four, so that every O row can be read 16 bytes at a time.
+__host__ __device__ inline int suffix_piece(int heads_per_pair) { return heads_per_pair * 128 + (heads_per_pair + 3) / 4 * 4; }
+struct SuffixPlan {
+    int heads_per_pair, head_groups;
+    long long units;  // at most: the lengths are read on the device
+    int ctas;
+    size_t piece_floats;
+};
+SuffixPlan suffix_plan(int B, int Hq, int Hkv, int max_seq_len, int sm_count);
+struct SuffixArgs {
+    const void *q, *k_pages, *v_pages;
+    const int *seq_lens, *block_table;
+    float *o, *lse, *pieces;
+    int B, Hq, Hkv, num_pages, page_size, pages_per_seq, cap;
+    float scale;
+    SuffixPlan plan;
+    int *status;
+};
+cudaError_t launch_suffix(const SuffixArgs &a, cudaStream_t stream, int *encode_error);
+
+// Joins the prefix's segments and the suffixes' results into o (bf16) and lse (natural log).
 struct PrefixMergeArgs {
     PrefixPlan plan;
     int B, Hq, Hkv, cap;
     const int *prefix_len;
     const float *part_o, *part_lse;
-    const float *o_suffix, *lse_suffix, *suffix_ws;  // null: no suffixes
-    DecodePlan suffix;
+    const float *o_suffix, *lse_suffix, *pieces;  // null: no suffixes
+    SuffixPlan suffix;
     const int *seq_lens;
     int suffix_cap;
     void *o;
@@ -280,9 +310,6 @@ constexpr int kPagedMaxBatch = 1024;  // batch entries a paged decode may have (
 // upper bounds (cpp from max_seq_len; total is computed by each CTA); every pair may be shared.
 cudaError_t decode_plan_paged(int B, int Hq, int Hkv, int max_seq_len, int requested_ctas, int sm_count,
                               DecodePlan *plan, bool fp8 = false);
-// Plan of the suffixes of a shared-prefix decode: pairs hold up to 16 heads of a group of any size, and
-// the pieces of shared pairs are left in the workspace (launched with o_part given).
-cudaError_t decode_plan_suffix(int B, int Hq, int Hkv, int max_seq_len, int sm_count, DecodePlan *plan);
 cudaError_t launch_decode_tc(const DecodeArgs &a, cudaStream_t stream);
 
 // The status word of attn_decode_noalloc's fixed scratch array on the current device, or nullptr

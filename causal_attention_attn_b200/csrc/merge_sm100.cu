@@ -100,20 +100,23 @@ namespace {
 
 // Attention of one row of a shared-prefix decode from its parts, all fp32 with LSEs in log2 units: the
 // segments of its list of prefix tiles (prefill_sm100.cu, decode_segment) and its suffix, whole or in
-// the pieces that the CTAs which shared its pair left (decode_tc_sm100.cu).
+// the pieces that the workers which shared its pair left (suffix_sm100.cu).
 //   M = max LSE_s,  O = sum 2^(LSE_s - M) O_s / W,  lse = (M + log2 W) ln 2,  W = sum 2^(LSE_s - M).
-// One warp per row: lane k looks up where part k lies and its LSE (both before any O is read), then
-// every lane adds its four channels over the parts, eight reads in flight. Bound by the latency of that
-// chain for few rows, by reading the parts (still in L2) for many. Where the parts lie follows from the
-// lengths alone and is computed before the wait for the kernels that write them. A row with no part (no
-// prefix, no suffix) gives O = 0 and lse = -inf.
+// kSplit warps take one row, each every kSplit-th part: lane i looks up where its i-th part lies and
+// its LSE (before any O is read), then each lane adds its four channels over the warp's parts, eight reads
+// in flight, and the warps' sums are joined in shared memory. Bound by the latency of that chain for few
+// rows (four warps a row: see the launch), by reading the parts, still in L2, for many. Where the parts lie follows from the lengths alone and is computed before the wait for
+// the kernels that write them. A row with no part (no prefix, no suffix) gives O = 0 and lse = -inf.
 constexpr int kMergeWarps = 4;
+constexpr int kMergeSplitRows = 1024;
 
+template <int kSplit>
 __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const PrefixMergeArgs a)
 {
     constexpr int kTile = 128, D = 128;
-    const int lane = threadIdx.x & 31;
-    const int row = blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+    static_assert(kSplit == 1 || kSplit == kMergeWarps, "a row has a warp or a block");
+    const int lane = threadIdx.x & 31, warp = kSplit == 1 ? 0 : threadIdx.x >> 5;
+    const int row = kSplit == 1 ? blockIdx.x * kMergeWarps + (threadIdx.x >> 5) : blockIdx.x;
     if (row >= a.B * a.Hq)
         return;
     const int b = row / a.Hq, h = row - b * a.Hq;
@@ -129,67 +132,64 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const Pr
         c0 = static_cast<int>(range.part_of(list * tiles));
         n_prefix = static_cast<int>(range.part_of((list + 1) * tiles - 1)) - c0 + 1;
     }
-    // Suffix: its pair's units among all pairs' chunks laid end to end, as decode_tc_kernel lays them.
-    int s0 = 0, n_suffix = 0, in_pair = 0;
-    long long s_total = 0, s_first = 0;
-    bool whole = false;
+    // Suffix: its pair's units among all pairs' units, as suffix_kernel lays them.
+    int s0 = 0, n_suffix = 0, in_pair = 0, first_piece = 0;
     if (a.o_suffix) {
-        const int group = a.Hq / a.Hkv, G = a.suffix.G, per_b = a.Hkv * a.suffix.head_groups;
-        long long before = 0, all = 0;
+        const int group = a.Hq / a.Hkv, per = a.suffix.heads_per_pair, pairs = a.Hkv * a.suffix.head_groups;
+        auto units_of = [&](int i) {
+            return (min(max(__ldg(a.seq_lens + i), 0), a.suffix_cap) + kSuffixUnitKeys - 1) / kSuffixUnitKeys;
+        };
+        int before = 0, all = 0;
         for (int i = lane; i < a.B; i += 32) {
-            const int chunks = (min(max(__ldg(a.seq_lens + i), 0), a.suffix_cap) + kTile - 1) / kTile;
-            all += chunks;
-            before += i < b ? chunks : 0;
+            const int u = units_of(i);
+            all += u;
+            before += i < b ? u : 0;
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             all += __shfl_xor_sync(0xffffffffu, all, o);
             before += __shfl_xor_sync(0xffffffffu, before, o);
         }
-        const int chunks = (min(max(__ldg(a.seq_lens + b), 0), a.suffix_cap) + kTile - 1) / kTile;
-        const int g = h / group, in_group = h - g * group;
-        in_pair = in_group % G;
-        s_total = all * per_b;
-        s_first = before * per_b + static_cast<long long>(g * a.suffix.head_groups + in_group / G) * chunks;
-        if (chunks > 0) {
-            s0 = static_cast<int>(((s_first + 1) * a.suffix.ctas - 1) / s_total);
-            n_suffix = static_cast<int>(((s_first + chunks) * a.suffix.ctas - 1) / s_total) - s0 + 1;
-            whole = n_suffix == 1;
+        const int units = units_of(b), g = h / group, in_group = h - g * group;
+        in_pair = in_group % per;
+        if (units > 0) {
+            const int total = all * pairs;
+            const int first = before * pairs + (g * a.suffix.head_groups + in_group / per) * units;
+            const EvenRange range(total, suffix_workers(total, a.suffix.ctas));
+            s0 = static_cast<int>(range.part_of(first));
+            n_suffix = static_cast<int>(range.part_of(first + units - 1)) - s0 + 1;
+            // The first worker's piece is its last one unless its range starts with the pair.
+            first_piece = static_cast<int>(range.begin(s0)) >= first ? 0 : 1;
         }
     }
     const int n = n_prefix + n_suffix;
-    const size_t stride = static_cast<size_t>(a.suffix.G) * (D + 1);  // one piece in suffix_ws
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    // Part k: its O row and its LSE; -inf where there is none.
+    // Part k: its O row and its LSE; -inf behind the last.
     auto part = [&](int k, const float **o) -> float {
         *o = a.part_o;
         if (k < n_prefix) {
-            const int c = c0 + k;
-            const long long r = (static_cast<long long>(list + c) * 2 + (tile & 1)) * kTile + in_tile;
+            const long long r = (static_cast<long long>(list + c0 + k) * 2 + (tile & 1)) * kTile + in_tile;
             *o = a.part_o + r * D;
             return __ldcg(a.part_lse + r);
         }
         if (k >= n)
             return -INFINITY;
-        if (whole) {
+        if (n_suffix == 1) {  // the whole pair
             *o = a.o_suffix + static_cast<size_t>(row) * D;
             return __ldcg(a.lse_suffix + row);
         }
-        const int c = s0 + k - n_prefix;
-        const long long begin = s_total * c / a.suffix.ctas;
-        if (begin >= s_total * (c + 1) / a.suffix.ctas)
-            return -INFINITY;
-        const float *piece = a.suffix_ws + (static_cast<size_t>(c) * 2 + (begin >= s_first ? 0 : 1)) * stride;
+        const int i = k - n_prefix, per = a.suffix.heads_per_pair;
+        const float *piece = a.pieces + (static_cast<size_t>(s0 + i) * 2 + (i == 0 ? first_piece : 0)) * suffix_piece(per);
         *o = piece + in_pair * D;
-        return __ldcg(piece + a.suffix.G * D + in_pair);
+        return __ldcg(piece + per * D + in_pair);
     };
     float M = -INFINITY, W = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < n; k += 32) {
+    for (int k = 0; k < n; k += 32 * kSplit) {
         const float *o;
-        const float l = part(k + lane, &o);
+        const float l = part(k + lane * kSplit + warp, &o);
         float m = l;
 #pragma unroll
         for (int s = 16; s > 0; s >>= 1)
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const Pr
         M = new_m;
         // fmaxf drops NaN: a part with a NaN LSE (from NaN scores) keeps a NaN weight.
         const float w = l == -INFINITY ? 0.f : exp2f(l - M);
-        const int parts = min(32, n - k);
+        const int parts = min(32, (n - k - warp + kSplit - 1) / kSplit);
         for (int t = 0; t < parts; t += 8) {
             float4 v[8];
             float wt[8];
@@ -211,37 +211,70 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const Pr
                 wt[j] = __shfl_sync(0xffffffffu, w, from);
                 const float *po = reinterpret_cast<const float *>(
                     __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), from));
-                // Behind the last part the weight is 0; an absent part's row is not read (it may hold NaN).
                 v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (t + j < parts && wt[j] != 0.f)
                     v[j] = __ldcg(reinterpret_cast<const float4 *>(po) + lane);
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                acc.x = fmaf(wt[j], v[j].x, acc.x);
-                acc.y = fmaf(wt[j], v[j].y, acc.y);
-                acc.z = fmaf(wt[j], v[j].z, acc.z);
-                acc.w = fmaf(wt[j], v[j].w, acc.w);
-                W += t + j < parts ? wt[j] : 0.f;
+                const float u = t + j < parts ? wt[j] : 0.f;
+                acc.x = fmaf(u, v[j].x, acc.x);
+                acc.y = fmaf(u, v[j].y, acc.y);
+                acc.z = fmaf(u, v[j].z, acc.z);
+                acc.w = fmaf(u, v[j].w, acc.w);
+                W += u;
             }
         }
     }
-    const float inv = W == 0.f ? 0.f : 1.f / W;  // 0 only for a row without parts
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-    uint2 out;
-    out.x = *reinterpret_cast<const uint32_t *>(&lo);
-    out.y = *reinterpret_cast<const uint32_t *>(&hi);
-    reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.o) + static_cast<size_t>(row) * D)[lane] = out;
-    if (lane == 0)
-        a.lse[row] = W == 0.f ? -INFINITY : (M + log2f(W)) * 0.6931471805599453f;
+    if constexpr (kSplit == 1) {
+        const float inv = W == 0.f ? 0.f : 1.f / W;  // 0 only for a row without parts
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+        uint2 out;
+        out.x = *reinterpret_cast<const uint32_t *>(&lo);
+        out.y = *reinterpret_cast<const uint32_t *>(&hi);
+        reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.o) + static_cast<size_t>(row) * D)[lane] = out;
+        if (lane == 0)
+            a.lse[row] = W == 0.f ? -INFINITY : (M + log2f(W)) * 0.6931471805599453f;
+        return;
+    }
+    __shared__ float s_acc[kMergeWarps][D];
+    __shared__ float s_m[kMergeWarps], s_w[kMergeWarps];
+    *reinterpret_cast<float4 *>(&s_acc[warp][4 * lane]) = acc;
+    if (lane == 0) {
+        s_m[warp] = M;
+        s_w[warp] = W;
+    }
+    __syncthreads();
+    const int d = threadIdx.x;  // one channel each
+    float top = s_m[0];
+#pragma unroll
+    for (int v = 1; v < kMergeWarps; ++v)
+        top = fmaxf(top, s_m[v]);
+    float sum = 0.f, out = 0.f;
+#pragma unroll
+    for (int v = 0; v < kMergeWarps; ++v) {
+        // A warp without parts has M = -inf and sums 0 (or NaN, which stays).
+        const float f = s_m[v] == top ? 1.f : exp2f(s_m[v] - top);
+        sum = fmaf(f, s_w[v], sum);
+        out = fmaf(f, s_acc[v][d], out);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // 0 only for a row without parts
+    static_cast<__nv_bfloat16 *>(a.o)[static_cast<size_t>(row) * D + d] = __float2bfloat16_rn(out * inv);
+    if (d == 0)
+        a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 }  // namespace
 
 cudaError_t launch_prefix_merge(const PrefixMergeArgs &a, cudaStream_t stream)
 {
+    static_assert(32 * kMergeWarps == 128, "one thread a channel");
     const int rows = a.B * a.Hq;
-    return launch_behind(prefix_merge_kernel, (rows + kMergeWarps - 1) / kMergeWarps, 32 * kMergeWarps, 0, stream, true, a);
+    // Up to a block an SM's worth of rows or so, latency counts; beyond it, the work a row costs.
+    if (rows <= kMergeSplitRows)
+        return launch_behind(prefix_merge_kernel<kMergeWarps>, rows, 32 * kMergeWarps, 0, stream, true, a);
+    return launch_behind(prefix_merge_kernel<1>, (rows + kMergeWarps - 1) / kMergeWarps, 32 * kMergeWarps, 0, stream, true, a);
 }
 
 }  // namespace attn_b200
