@@ -43,6 +43,8 @@ class AttnError(RuntimeError):
 def load_library(path: str | None = None):
     """Load the library once. Raises if it has not been built."""
     global _lib
+    if _lib is not None and path is None:
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib
@@ -506,8 +508,9 @@ def attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
 
 _NORM_ROPE_BWD_BLOCKS = 592  # ATTN_QK_NORM_ROPE_BWD_WORKSPACE(D) holds two rows of D floats for each
 
-# The calls below come once per layer and token, so the host's time counts: a call's tensors are
-# checked with as few torch calls as the checks need.
+# The calls below come once per layer and token, so the host's time counts: each tensor is checked
+# with as few torch calls as the checks need, and only a tensor that fails them is looked at again to
+# say what is wrong.
 
 
 @functools.lru_cache(maxsize=1024)
@@ -516,17 +519,37 @@ def _stride_array(b: int, h: int, s: int):
     return (ctypes.c_longlong * 3)(b, h, s)
 
 
-def _rows_strides(t, shape):
-    """As ``_strides3`` of a [B, H, S, D] tensor whose shape is at hand."""
-    b, h, s, _ = t.stride()
-    B, H, S, D = shape
-    return _stride_array(b if B > 1 else D, h if H > 1 else D, s if S > 1 else D)
+def _device_of(name, t):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    return t.get_device()
 
 
-def _same_device(index, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.get_device() != index:
-            raise ValueError(f"{name} must live on cuda:{index}, got {t.device}")
+def _flat(name, t, dtype, ndim, dev):
+    """The shape of a contiguous tensor of this type and rank on device `dev`."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev >= 0 and t.is_contiguous():
+        shape = t.shape
+        if len(shape) == ndim:
+            return shape
+    _check_tensor(name, t, dtype, ndim)
+    raise ValueError(f"{name} must live on cuda:{dev}, got {t.device}")
+
+
+def _rows(name, t, dev, like=None):
+    """The shape and the stride array of a bf16 [batch, head, row, dim] view with a contiguous dim on
+    device `dev`; with `like`, of that shape."""
+    if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.get_device() == dev >= 0:
+        strides = t.stride()
+        if len(strides) == 4 and strides[3] == 1:
+            B, H, S, D = shape = t.shape
+            if like is not None and shape != like:
+                raise ValueError(f"{name} must have the shape {tuple(like)}, got {tuple(shape)}")
+            # An axis of extent 1 gets D: its stride is never used, and the library wants a multiple of 8.
+            return shape, _stride_array(strides[0] if B > 1 else D, strides[1] if H > 1 else D, strides[2] if S > 1 else D)
+    _check_rows(name, t, torch.bfloat16)
+    if t.shape[-1] == 1:
+        raise ValueError(f"{name} has a head dim of 1")
+    raise ValueError(f"{name} must live on cuda:{dev}, got {t.device}")
 
 
 class _Launch:
@@ -551,42 +574,45 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _check_rotation(cos, sin, D):
+def _rotation(cos, sin, D, dev):
     """(rot_dim, max_pos) of the angle tables cos, sin [max_pos, rot_dim / 2]; (0, 0) without them."""
     if cos is None and sin is None:
         return 0, 0
-    _check_tensor("cos", cos, torch.float32, 2)
-    _check_tensor("sin", sin, torch.float32, 2)
-    max_pos, half = shape = cos.shape
-    if sin.shape != shape:
+    max_pos, half = shape = _flat("cos", cos, torch.float32, 2, dev)
+    if _flat("sin", sin, torch.float32, 2, dev) != shape:
         raise ValueError(f"cos {tuple(cos.shape)} and sin {tuple(sin.shape)} must agree")
     if 2 * half > D:
         raise ValueError(f"the tables rotate {2 * half} channels of a head of {D}")
     return 2 * half, max_pos
 
 
-def _check_weights(q_weight, k_weight, D):
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _check_tensor(name, w, torch.bfloat16, 1)
-            if w.shape[0] != D:
-                raise ValueError(f"{name} must be [{D}], got {tuple(w.shape)}")
+def _weight(name, w, D, dev):
+    if w is None:
+        return None
+    if _flat(name, w, torch.bfloat16, 1, dev)[0] != D:
+        raise ValueError(f"{name} must be [{D}], got {tuple(w.shape)}")
+    return w.data_ptr()
 
 
-def _check_positions(positions, B, S):
-    if positions is not None:
-        _check_tensor("positions", positions, torch.int32, 2)
-        if tuple(positions.shape) != (B, S):
-            raise ValueError(f"positions must be [{B}, {S}], got {tuple(positions.shape)}")
+def _positions(positions, B, S, dev):
+    if positions is None:
+        return None
+    if _flat("positions", positions, torch.int32, 2, dev) != (B, S):
+        raise ValueError(f"positions must be [{B}, {S}], got {tuple(positions.shape)}")
+    return positions.data_ptr()
 
 
-def _out_rows(name, t, like):
-    if t is None:
-        return torch.empty(like.shape, dtype=torch.bfloat16, device=like.device)
-    _check_rows(name, t, torch.bfloat16)
-    if t.shape != like.shape:
-        raise ValueError(f"{name} must have the shape {tuple(like.shape)}")
-    return t
+def _new_rows(like):
+    return torch.empty(like.shape, dtype=torch.bfloat16, device=like.device)
+
+
+def _used_on(stream, *tensors):
+    """Memory that this module allocated and a stream other than the current one uses: the caching
+    allocator may hand it out again only behind that stream."""
+    if stream is not None:
+        used = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+        for t in tensors:
+            t.record_stream(used)
 
 
 def attn_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor | None, sin: torch.Tensor | None,
@@ -601,25 +627,23 @@ def attn_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor | None
     token-major projection, say); cos, sin fp32 [max_pos, rot_dim / 2], or None for both: no rotation;
     q_weight, k_weight bf16 [D], both or neither; positions int32 [B, S] (default: the row index).
     Returns (q_out, k_out), heads-major contiguous unless given; an output may be its input."""
-    _check_rows("q", q, torch.bfloat16)
-    _check_rows("k", k, torch.bfloat16)
-    B, Hq, S, D = qshape = q.shape
-    Bk, Hkv, Sk, Dk = kshape = k.shape
+    dev = _device_of("q", q)
+    qshape, qs = _rows("q", q, dev)
+    kshape, ks = _rows("k", k, dev)
+    B, Hq, S, D = qshape
+    Bk, Hkv, Sk, Dk = kshape
     if Bk != B or Sk != S or Dk != D:
         raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}")
-    rot_dim, max_pos = _check_rotation(cos, sin, D)
-    _check_weights(q_weight, k_weight, D)
-    _check_positions(positions, B, S)
-    q_out, k_out = _out_rows("q_out", q_out, q), _out_rows("k_out", k_out, k)
-    dev = q.get_device()
-    _same_device(dev, k=k, cos=cos, sin=sin, q_weight=q_weight, k_weight=k_weight, positions=positions, q_out=q_out,
-                 k_out=k_out)
+    rot_dim, max_pos = _rotation(cos, sin, D, dev)
+    qw, kw, pos = _weight("q_weight", q_weight, D, dev), _weight("k_weight", k_weight, D, dev), _positions(positions, B, S, dev)
+    q_out = _new_rows(q) if q_out is None else q_out
+    k_out = _new_rows(k) if k_out is None else k_out
+    _, qos = _rows("q_out", q_out, dev, qshape)
+    _, kos = _rows("k_out", k_out, dev, kshape)
     with _Launch(dev, stream) as handle:
         rc = load_library().attn_qk_norm_rope(
-            q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(positions),
-            q_out.data_ptr(), k_out.data_ptr(), B, Hq, Hkv, S, D, _rows_strides(q, qshape), _rows_strides(k, kshape),
-            _rows_strides(q_out, qshape), _rows_strides(k_out, kshape), rot_dim, max_pos, 1 if interleaved else 0, eps,
-            handle)
+            q.data_ptr(), k.data_ptr(), qw, kw, _ptr(cos), _ptr(sin), pos, q_out.data_ptr(), k_out.data_ptr(), B, Hq, Hkv,
+            S, D, qs, ks, qos, kos, rot_dim, max_pos, 1 if interleaved else 0, eps, handle)
     _check(rc)
     return q_out, k_out
 
@@ -633,39 +657,32 @@ def attn_qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor | 
     gradients of its outputs (``attn_bwd``'s dq and dk), q, k and the rest its inputs. dq, dk may be
     views (slices of a fused projection's gradient). Returns (dq, dk, dq_weight, dk_weight), the last
     two fp32 [D], or None without weights."""
-    _check_rows("q", q, torch.bfloat16)
-    _check_rows("k", k, torch.bfloat16)
-    _check_rows("dq_out", dq_out, torch.bfloat16)
-    _check_rows("dk_out", dk_out, torch.bfloat16)
-    B, Hq, S, D = qshape = q.shape
-    Bk, Hkv, Sk, Dk = kshape = k.shape
-    if Bk != B or Sk != S or Dk != D or dq_out.shape != qshape or dk_out.shape != kshape:
-        raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}, dq_out {tuple(dq_out.shape)}, "
-                         f"dk_out {tuple(dk_out.shape)}")
-    rot_dim, max_pos = _check_rotation(cos, sin, D)
-    _check_weights(q_weight, k_weight, D)
-    _check_positions(positions, B, S)
-    dq, dk = _out_rows("dq", dq, q), _out_rows("dk", dk, k)
-    dev = q.get_device()
-    _same_device(dev, k=k, cos=cos, sin=sin, dq_out=dq_out, dk_out=dk_out, q_weight=q_weight, k_weight=k_weight,
-                 positions=positions, dq=dq, dk=dk)
+    dev = _device_of("q", q)
+    qshape, qs = _rows("q", q, dev)
+    kshape, ks = _rows("k", k, dev)
+    B, Hq, S, D = qshape
+    Bk, Hkv, Sk, Dk = kshape
+    if Bk != B or Sk != S or Dk != D:
+        raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}")
+    _, dqos = _rows("dq_out", dq_out, dev, qshape)
+    _, dkos = _rows("dk_out", dk_out, dev, kshape)
+    rot_dim, max_pos = _rotation(cos, sin, D, dev)
+    qw, kw, pos = _weight("q_weight", q_weight, D, dev), _weight("k_weight", k_weight, D, dev), _positions(positions, B, S, dev)
+    dq = _new_rows(q) if dq is None else dq
+    dk = _new_rows(k) if dk is None else dk
+    _, dqs = _rows("dq", dq, dev, qshape)
+    _, dks = _rows("dk", dk, dev, kshape)
     dwq = dwk = ws = None
     with _Launch(dev, stream) as handle:
-        if q_weight is not None:
-            # One block for the weights' gradients (two views of 16-byte aligned rows) and one that the
-            # kernels use and nobody else: the caching allocator hands it out again behind this stream.
+        if qw is not None:
+            # One block for the weights' gradients (rows of 16-byte aligned floats), one for the kernels.
             dwq, dwk = torch.empty((2, D), dtype=torch.float32, device=q.device).unbind(0)
             ws = torch.empty((_NORM_ROPE_BWD_BLOCKS * 2 * D,), dtype=torch.float32, device=q.device)
-            if stream is not None:
-                used = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
-                for t in (dwq, ws):
-                    t.record_stream(used)
+            _used_on(stream, dwq, ws)
         rc = load_library().attn_qk_norm_rope_bwd(
-            q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(positions),
-            dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), _ptr(dwq), _ptr(dwk), _ptr(ws), B, Hq,
-            Hkv, S, D, _rows_strides(q, qshape), _rows_strides(k, kshape), _rows_strides(dq_out, qshape),
-            _rows_strides(dk_out, kshape), _rows_strides(dq, qshape), _rows_strides(dk, kshape), rot_dim, max_pos,
-            1 if interleaved else 0, eps, handle)
+            q.data_ptr(), k.data_ptr(), qw, kw, _ptr(cos), _ptr(sin), pos, dq_out.data_ptr(), dk_out.data_ptr(),
+            dq.data_ptr(), dk.data_ptr(), _ptr(dwq), _ptr(dwk), _ptr(ws), B, Hq, Hkv, S, D, qs, ks, dqos, dkos, dqs, dks,
+            rot_dim, max_pos, 1 if interleaved else 0, eps, handle)
     _check(rc)
     return dq, dk, dwq, dwk
 
@@ -673,56 +690,44 @@ def attn_qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor | 
 def _append(k, v, cos, sin, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, q, q_out, q_weight, k_weight,
             positions, new_lens, interleaved, eps, stream):
     fp8 = k_scale is not None
-    _check_rows("k", k, torch.bfloat16)
-    _check_rows("v", v, torch.bfloat16)
+    dev = _device_of("k", k)
+    shape, ks = _rows("k", k, dev)
+    _, vs = _rows("v", v, dev, shape)
     if fp8:
         k_pages, v_pages = _as_codes("k_pages", k_pages), _as_codes("v_pages", v_pages)
-    else:
-        _check_tensor("k_pages", k_pages, torch.bfloat16, 4)
-        _check_tensor("v_pages", v_pages, torch.bfloat16, 4)
-    _check_tensor("block_table", block_table, torch.int32, 2)
-    _check_tensor("seq_lens", seq_lens, torch.int32, 1)
-    B, Hkv, Sq, D = shape = k.shape
-    num_pages, Hp, page_size, Dp = pages = k_pages.shape
-    if v.shape != shape or v_pages.shape != pages or Hp != Hkv or D != 128 or Dp != D:
+    cache = torch.uint8 if fp8 else torch.bfloat16
+    B, Hkv, Sq, D = shape
+    num_pages, Hp, page_size, Dp = pages = _flat("k_pages", k_pages, cache, 4, dev)
+    if _flat("v_pages", v_pages, cache, 4, dev) != pages or Hp != Hkv or D != 128 or Dp != D:
         raise ValueError(f"expected k, v [B,Hkv,Sq,128] and pages [P,Hkv,page,128]; got {tuple(k.shape)}, "
                          f"{tuple(v.shape)}, {tuple(k_pages.shape)}, {tuple(v_pages.shape)}")
-    rows, per_seq = block_table.shape
-    if rows != B or seq_lens.shape[0] != B:
+    rows, per_seq = _flat("block_table", block_table, torch.int32, 2, dev)
+    if rows != B or _flat("seq_lens", seq_lens, torch.int32, 1, dev)[0] != B:
         raise ValueError("block_table and seq_lens need one row / entry per batch element")
-    if new_lens is not None:
-        _check_tensor("new_lens", new_lens, torch.int32, 1)
-        if new_lens.shape[0] != B:
-            raise ValueError("new_lens needs one entry per batch element")
+    if new_lens is not None and _flat("new_lens", new_lens, torch.int32, 1, dev)[0] != B:
+        raise ValueError("new_lens needs one entry per batch element")
     if fp8:
         for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-            _check_tensor(name, t, torch.float32, 2)
-            if tuple(t.shape) != (Hkv, D):
+            if _flat(name, t, torch.float32, 2, dev) != (Hkv, D):
                 raise ValueError(f"{name} must be [{Hkv}, {D}], got {tuple(t.shape)}")
-    rot_dim, max_pos = _check_rotation(cos, sin, D)
-    _check_weights(q_weight, k_weight, D)
-    _check_positions(positions, B, Sq)
+    rot_dim, max_pos = _rotation(cos, sin, D, dev)
+    qw, kw, pos = _weight("q_weight", q_weight, D, dev), _weight("k_weight", k_weight, D, dev), _positions(positions, B, Sq, dev)
     Hq, qs, qos = 0, None, None
     if q is not None:
-        _check_rows("q", q, torch.bfloat16)
-        Bq, Hq, S, Dq = qshape = q.shape
+        qshape, qs = _rows("q", q, dev)
+        Bq, Hq, S, Dq = qshape
         if Bq != B or S != Sq or Dq != D:
             raise ValueError(f"q must be [{B}, Hq, {Sq}, {D}], got {tuple(q.shape)}")
-        q_out = _out_rows("q_out", q_out, q)
-        qs, qos = _rows_strides(q, qshape), _rows_strides(q_out, qshape)
+        q_out = _new_rows(q) if q_out is None else q_out
+        _, qos = _rows("q_out", q_out, dev, qshape)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    dev = k.get_device()
-    _same_device(dev, v=v, q=q, q_out=q_out, cos=cos, sin=sin, k_pages=k_pages, v_pages=v_pages, k_scale=k_scale,
-                 v_scale=v_scale, block_table=block_table, seq_lens=seq_lens, new_lens=new_lens, positions=positions,
-                 q_weight=q_weight, k_weight=k_weight)
     lib = load_library()
-    head = (_ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin),
-            _ptr(positions), seq_lens.data_ptr(), _ptr(new_lens), block_table.data_ptr(), _ptr(q_out),
-            k_pages.data_ptr(), v_pages.data_ptr())
+    head = (_ptr(q), k.data_ptr(), v.data_ptr(), qw, kw, _ptr(cos), _ptr(sin), pos, seq_lens.data_ptr(),
+            _ptr(new_lens), block_table.data_ptr(), _ptr(q_out), k_pages.data_ptr(), v_pages.data_ptr())
     with _Launch(dev, stream) as handle:
-        tail = (B, Hq, Hkv, Sq, qs, _rows_strides(k, shape), _rows_strides(v, shape), qos, num_pages, page_size,
-                per_seq, rot_dim, max_pos, 1 if interleaved else 0, eps, handle)
+        tail = (B, Hq, Hkv, Sq, qs, ks, vs, qos, num_pages, page_size, per_seq, rot_dim, max_pos,
+                1 if interleaved else 0, eps, handle)
         if fp8:
             rc = lib.attn_append_paged_fp8(*head, k_scale.data_ptr(), v_scale.data_ptr(), *tail)
         else:
@@ -790,44 +795,32 @@ def attn_decode_prefix(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Te
     the keys behind the prefix (all on the GPU); max_prefix_len, max_seq_len: host-side bounds of the
     lengths. ``workspace`` from ``decode_prefix_workspace`` keeps a loop of calls from allocating.
     Returns (o [B, Hq, 1, 128], lse [B, Hq, 1])."""
-    _check_tensor("q", q, torch.bfloat16, 4)
-    _check_tensor("k_pages", k_pages, torch.bfloat16, 4)
-    _check_tensor("v_pages", v_pages, torch.bfloat16, 4)
-    _check_tensor("prefix_table", prefix_table, torch.int32, 1)
-    _check_tensor("prefix_len", prefix_len, torch.int32, 1)
-    _check_tensor("block_table", block_table, torch.int32, 2)
-    _check_tensor("seq_lens", seq_lens, torch.int32, 1)
-    B, Hq, Sq, D = qshape = q.shape
-    num_pages, Hkv, page_size, Dk = pages = k_pages.shape
-    if Sq != 1 or v_pages.shape != pages or Dk != D or D != 128:
+    dev = _device_of("q", q)
+    B, Hq, Sq, D = qshape = _flat("q", q, torch.bfloat16, 4, dev)
+    num_pages, Hkv, page_size, Dk = pages = _flat("k_pages", k_pages, torch.bfloat16, 4, dev)
+    if Sq != 1 or _flat("v_pages", v_pages, torch.bfloat16, 4, dev) != pages or Dk != D or D != 128:
         raise ValueError(f"expected q [B,Hq,1,128] and k, v pages [P,Hkv,page,128]; got {tuple(q.shape)}, "
                          f"{tuple(k_pages.shape)}, {tuple(v_pages.shape)}")
-    rows, per_seq = block_table.shape
-    if rows != B or seq_lens.shape[0] != B or prefix_len.shape[0] != 1:
+    prefix_pages, = _flat("prefix_table", prefix_table, torch.int32, 1, dev)
+    rows, per_seq = _flat("block_table", block_table, torch.int32, 2, dev)
+    if rows != B or _flat("seq_lens", seq_lens, torch.int32, 1, dev)[0] != B \
+            or _flat("prefix_len", prefix_len, torch.int32, 1, dev)[0] != 1:
         raise ValueError("block_table and seq_lens need one row / entry per batch element, prefix_len one entry")
     if scale is None:
         scale = D ** -0.5
     out = torch.empty(qshape, dtype=torch.bfloat16, device=q.device) if out is None else out
     lse = torch.empty((B, Hq, 1), dtype=torch.float32, device=q.device) if lse is None else lse
-    _check_tensor("out", out, torch.bfloat16, 4)
-    _check_tensor("lse", lse, torch.float32, 3)
-    if out.shape != qshape or lse.shape != (B, Hq, 1):
+    if _flat("out", out, torch.bfloat16, 4, dev) != qshape or _flat("lse", lse, torch.float32, 3, dev) != (B, Hq, 1):
         raise ValueError(f"out must be {tuple(qshape)} and lse {(B, Hq, 1)}")
-    dev = q.get_device()
     if workspace is None:
-        workspace = decode_prefix_workspace(B, Hq, Hkv, int(max_prefix_len), int(max_seq_len), q.device)
-        if stream is not None:
-            workspace.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
-    else:
-        _check_tensor("workspace", workspace, torch.uint8, 1)
-    _same_device(dev, k_pages=k_pages, v_pages=v_pages, prefix_table=prefix_table, prefix_len=prefix_len,
-                 block_table=block_table, seq_lens=seq_lens, out=out, lse=lse, workspace=workspace)
+        workspace = decode_prefix_workspace(B, Hq, Hkv, max_prefix_len, max_seq_len, q.device)
+        _used_on(stream, workspace)
+    ws_bytes, = _flat("workspace", workspace, torch.uint8, 1, dev)
     with _Launch(dev, stream) as handle:
         rc = load_library().attn_decode_prefix(
             q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), prefix_table.data_ptr(), prefix_len.data_ptr(),
-            block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-            workspace.shape[0], B, Hq, Hkv, num_pages, page_size, int(prefix_table.shape[0]), max_prefix_len, per_seq,
-            max_seq_len, scale, handle)
+            block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), ws_bytes,
+            B, Hq, Hkv, num_pages, page_size, prefix_pages, max_prefix_len, per_seq, max_seq_len, scale, handle)
     _check(rc)
     return out, lse
 

@@ -779,6 +779,24 @@ int plan_prefix(const DeviceState &s, int B, int Hq, int Hkv, int max_prefix_len
 {
     *pl = prefix_plan(B, Hq, Hkv, max_prefix_len, s.sm_count);
     *suffix = suffix_plan(B, Hq, Hkv, max_seq_len, s.sm_count);
+    if (max_seq_len > 0 && max_prefix_len > 0) {
+        // Side by side where that costs the prefix little: with n KV tiles to a CTA it needs ceil(units /
+        // n) SMs, and the rest take the suffixes if they are done with them before. Measured: the prefix's
+        // kernel takes 4.5 us and 1.6 us a KV tile (2.0 with two query tiles), the suffixes' 3.4 us and
+        // 0.112 us for each unit of an SM (8 KB at 73 GB/s); in turn the suffixes cost 4 us at the least, so
+        // the prefix may lose that much. Both lengths are bounds here: a shorter suffix leaves SMs idle
+        // that the prefix did without.
+        const long long n0 = (pl->units + s.sm_count - 1) / s.sm_count;
+        const double tile_us = pl->tile_pairs * pl->tile_seqs >= B ? 1.6 : 2.0;
+        for (long long n = n0; tile_us * static_cast<double>(n - n0) < 4.0; ++n) {
+            const int ctas = static_cast<int>((pl->units + n - 1) / n), rest = s.sm_count - ctas;
+            if (rest < 1 || 3.4 + 0.112 * static_cast<double>(suffix->units) / rest > 4.5 + tile_us * static_cast<double>(n))
+                continue;
+            *pl = prefix_plan(B, Hq, Hkv, max_prefix_len, ctas);
+            *suffix = suffix_plan(B, Hq, Hkv, max_seq_len, rest);
+            break;
+        }
+    }
     if (pl->slots * 256 > INT_MAX)
         return ATTN_ERR_SHAPE;
     *sp = prefix_space(B, Hq, *pl, *suffix);
@@ -860,10 +878,32 @@ extern "C" int attn_decode_prefix(const void *q, const void *k_pages, const void
         s->prefix_status = static_cast<int *>(word);
     }
     auto at = [&](size_t off) { return static_cast<char *>(workspace) + off; };
-    // The suffixes first: the prefix's kernel needs nothing of theirs and starts on the SMs that they
-    // leave free; the merge waits for both.
-    const bool own = max_seq_len > 0;
+    // The suffixes' kernel needs nothing of the prefix's and starts on the SMs that it leaves free; the
+    // merge waits for both.
+    PrefixArgs pa;
+    pa.q = q;
+    pa.k_pages = k_pages;
+    pa.v_pages = v_pages;
+    pa.prefix_table = prefix_table;
+    pa.prefix_len = prefix_len;
+    pa.B = B;
+    pa.Hq = Hq;
+    pa.Hkv = Hkv;
+    pa.num_pages = num_pages;
+    pa.page_size = page_size;
+    pa.prefix_pages = prefix_pages;
+    pa.max_prefix_len = max_prefix_len;
+    pa.scale = scale;
+    pa.plan = pl;
+    pa.part_o = reinterpret_cast<float *>(at(sp.part_o));
+    pa.part_lse = reinterpret_cast<float *>(at(sp.part_lse));
+    pa.status = s->prefix_status;
     int encode_error = 0;
+    if (launch_prefix(pa, stream, &encode_error) != cudaSuccess) {
+        cudaGetLastError();
+        return encode_error ? ATTN_ERR_CUDA : ATTN_ERR_LAUNCH;
+    }
+    const bool own = max_seq_len > 0;
     if (own) {
         SuffixArgs a;
         a.q = q;
@@ -888,29 +928,6 @@ extern "C" int attn_decode_prefix(const void *q, const void *k_pages, const void
             cudaGetLastError();
             return encode_error ? ATTN_ERR_CUDA : ATTN_ERR_LAUNCH;
         }
-    }
-    PrefixArgs pa;
-    pa.q = q;
-    pa.k_pages = k_pages;
-    pa.v_pages = v_pages;
-    pa.prefix_table = prefix_table;
-    pa.prefix_len = prefix_len;
-    pa.B = B;
-    pa.Hq = Hq;
-    pa.Hkv = Hkv;
-    pa.num_pages = num_pages;
-    pa.page_size = page_size;
-    pa.prefix_pages = prefix_pages;
-    pa.max_prefix_len = max_prefix_len;
-    pa.scale = scale;
-    pa.plan = pl;
-    pa.part_o = reinterpret_cast<float *>(at(sp.part_o));
-    pa.part_lse = reinterpret_cast<float *>(at(sp.part_lse));
-    pa.status = s->prefix_status;
-    pa.behind_suffix = own;
-    if (launch_prefix(pa, stream, &encode_error) != cudaSuccess) {
-        cudaGetLastError();
-        return encode_error ? ATTN_ERR_CUDA : ATTN_ERR_LAUNCH;
     }
     PrefixMergeArgs m;
     m.plan = pl;

@@ -6,6 +6,8 @@
 
 #include <cuda_runtime.h>
 
+#include "fast_div.h"
+
 namespace attn_b200 {
 
 // Devices the library keeps state for (function attributes, occupancy, workspaces), by index.
@@ -35,7 +37,11 @@ cudaError_t launch_behind(void (*kernel)(Params...), int grid, int threads, size
 // total % parts are the longer ones): with fewer units than parts the last ranges are empty.
 struct EvenRange {
     unsigned base, rem;
-    __host__ __device__ EvenRange(unsigned total, unsigned parts) : base(total / parts), rem(total % parts) {}
+    __host__ __device__ EvenRange(unsigned total, unsigned parts) : base(total / parts), rem(total - base * parts) {}
+    __host__ __device__ EvenRange(unsigned total, const FastDiv &parts)  // total < 2^31
+        : base(parts.quot(total)), rem(total - base * parts.d)
+    {
+    }
     __host__ __device__ unsigned begin(unsigned c) const { return c * base + (c < rem ? c : rem); }
     // The range that holds unit g < total.
     __host__ __device__ unsigned part_of(unsigned g) const
@@ -170,9 +176,11 @@ struct PrefixPlan {
     int tile_seqs;          // sequences in a tile
     int tile_pairs;         // per head
     long long lists, slots;
+    long long units;        // KV tiles of all lists, at most
     int ctas;
 };
-PrefixPlan prefix_plan(int B, int Hq, int Hkv, int max_prefix_len, int sm_count);
+// `ctas`: the most to launch.
+PrefixPlan prefix_plan(int B, int Hq, int Hkv, int max_prefix_len, int ctas);
 struct PrefixArgs {
     const void *q, *k_pages, *v_pages;
     const int *prefix_table, *prefix_len;  // [prefix_pages], [1]
@@ -181,7 +189,6 @@ struct PrefixArgs {
     PrefixPlan plan;
     float *part_o, *part_lse;
     int *status;
-    bool behind_suffix;  // launched right behind the suffixes' kernel: may overlap it
 };
 cudaError_t launch_prefix(const PrefixArgs &a, cudaStream_t stream, int *encode_error);
 
@@ -207,7 +214,7 @@ struct SuffixPlan {
     int ctas;
     size_t piece_floats;
 };
-SuffixPlan suffix_plan(int B, int Hq, int Hkv, int max_seq_len, int sm_count);
+SuffixPlan suffix_plan(int B, int Hq, int Hkv, int max_seq_len, int ctas);
 struct SuffixArgs {
     const void *q, *k_pages, *v_pages;
     const int *seq_lens, *block_table;
@@ -217,6 +224,7 @@ struct SuffixArgs {
     SuffixPlan plan;
     int *status;
 };
+// Launched right behind launch_prefix, which it may overlap.
 cudaError_t launch_suffix(const SuffixArgs &a, cudaStream_t stream, int *encode_error);
 
 // Joins the prefix's segments and the suffixes' results into o (bf16) and lse (natural log).
@@ -231,6 +239,7 @@ struct PrefixMergeArgs {
     int suffix_cap;
     void *o;
     float *lse;
+    FastDiv by_hq, by_tile_seqs, by_tile_group, by_group, by_pair, by_ctas;  // set by launch_prefix_merge
 };
 cudaError_t launch_prefix_merge(const PrefixMergeArgs &a, cudaStream_t stream);
 

@@ -119,23 +119,23 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const Pr
     const int row = kSplit == 1 ? blockIdx.x * kMergeWarps + (threadIdx.x >> 5) : blockIdx.x;
     if (row >= a.B * a.Hq)
         return;
-    const int b = row / a.Hq, h = row - b * a.Hq;
+    const int b = a.by_hq.quot(row), h = row - b * a.Hq;
 
     // Prefix: the CTAs from the one that holds the list's first unit to the one that holds its last.
-    const int tile = b / a.plan.tile_seqs;
-    const int in_tile = (b - tile * a.plan.tile_seqs) * a.plan.group + h % a.plan.group;
-    const int list = h / a.plan.group * a.plan.tile_pairs + tile / 2;
+    const int tile = a.by_tile_seqs.quot(b), part_of_heads = a.by_tile_group.quot(h);
+    const int in_tile = (b - tile * a.plan.tile_seqs) * a.plan.group + h - part_of_heads * a.plan.group;
+    const int list = part_of_heads * a.plan.tile_pairs + tile / 2;
     const int tiles = (min(max(__ldg(a.prefix_len), 0), a.cap) + kTile - 1) / kTile;
     int c0 = 0, n_prefix = 0;
     if (tiles > 0) {
-        const EvenRange range(static_cast<unsigned>(a.plan.lists) * tiles, a.plan.ctas);
+        const EvenRange range(static_cast<unsigned>(a.plan.lists) * tiles, a.by_ctas);
         c0 = static_cast<int>(range.part_of(list * tiles));
         n_prefix = static_cast<int>(range.part_of((list + 1) * tiles - 1)) - c0 + 1;
     }
     // Suffix: its pair's units among all pairs' units, as suffix_kernel lays them.
     int s0 = 0, n_suffix = 0, in_pair = 0, first_piece = 0;
     if (a.o_suffix) {
-        const int group = a.Hq / a.Hkv, per = a.suffix.heads_per_pair, pairs = a.Hkv * a.suffix.head_groups;
+        const int group = a.by_group.d, per = a.suffix.heads_per_pair, pairs = a.Hkv * a.suffix.head_groups;
         auto units_of = [&](int i) {
             return (min(max(__ldg(a.seq_lens + i), 0), a.suffix_cap) + kSuffixUnitKeys - 1) / kSuffixUnitKeys;
         };
@@ -150,11 +150,12 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const Pr
             all += __shfl_xor_sync(0xffffffffu, all, o);
             before += __shfl_xor_sync(0xffffffffu, before, o);
         }
-        const int units = units_of(b), g = h / group, in_group = h - g * group;
-        in_pair = in_group % per;
+        const int units = units_of(b), g = a.by_group.quot(h), in_group = h - g * group;
+        const int pair = a.by_pair.quot(in_group);
+        in_pair = in_group - pair * per;
         if (units > 0) {
             const int total = all * pairs;
-            const int first = before * pairs + (g * a.suffix.head_groups + in_group / per) * units;
+            const int first = before * pairs + (g * a.suffix.head_groups + pair) * units;
             const EvenRange range(total, suffix_workers(total, a.suffix.ctas));
             s0 = static_cast<int>(range.part_of(first));
             n_suffix = static_cast<int>(range.part_of(first + units - 1)) - s0 + 1;
@@ -267,8 +268,15 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const Pr
 
 }  // namespace
 
-cudaError_t launch_prefix_merge(const PrefixMergeArgs &a, cudaStream_t stream)
+cudaError_t launch_prefix_merge(const PrefixMergeArgs &args, cudaStream_t stream)
 {
+    PrefixMergeArgs a = args;
+    a.by_hq = FastDiv(a.Hq);
+    a.by_tile_seqs = FastDiv(a.plan.tile_seqs);
+    a.by_tile_group = FastDiv(a.plan.group);
+    a.by_group = FastDiv(a.Hq / a.Hkv);
+    a.by_pair = FastDiv(a.suffix.heads_per_pair);
+    a.by_ctas = FastDiv(a.plan.ctas);
     static_assert(32 * kMergeWarps == 128, "one thread a channel");
     const int rows = a.B * a.Hq;
     // Up to a block an SM's worth of rows or so, latency counts; beyond it, the work a row costs.

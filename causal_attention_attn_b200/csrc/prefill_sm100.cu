@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         if (warp == 11 && lane == 0)
             s_segments = find_segments(p);
-        asm volatile("griddepcontrol.launch_dependents;");  // the merge, which waits for this grid's end
+        asm volatile("griddepcontrol.launch_dependents;");  // the suffixes' kernel: it needs nothing of this one
     }
     if (warp == kWarpTma && lane == 0) {
         tma_prefetch_desc(&tm_q);
@@ -958,13 +958,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Partials: normalised O in fp32, 32 dims at a time turned in the warp's staging box (16-byte
                 // units XOR row % 8) so that eight lanes store one row's 128 bytes, and the LSE in log2
                 // units. (TMA stores from the box, waiting for each to be read, took 1.9 us a tile.)
-                // Rows behind the last sequence are written too (the slot has room) and never read.
+                // Only rows of sequences: an SM stores 32 bytes a cycle, so a full tile's 64 KB take a good us.
                 float *box = reinterpret_cast<float *>(smem + C::kOffStage + warp * C::kWarpStageBytes);
                 const int row0 = (cur.slot * 2 + x) * kBM + 32 * (warp & 3);
                 float *dst = p.part_o + static_cast<size_t>(row0) * D;
                 const int rr = lane >> 3, uu = lane & 7;
-#pragma unroll
-                for (int h = 0; h < D / 32; ++h) {
+                const int rows = min(p.tile_seqs, p.B - q0) * p.group - 32 * (warp & 3);  // of this warp's 32
+#pragma unroll 1  // once a segment: less code to fetch counts for more
+                for (int h = 0; h < (rows > 0 ? D / 32 : 0); ++h) {
                     uint32_t ov[32];
                     tmem_ld32_wait(tO + h * 32, ov);
                     __syncwarp();  // the rows of the 32 dims before are read
@@ -978,10 +979,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int t = 0; t < 8; ++t) {
                         const int r4 = 4 * t + rr;
                         const float4 v = *reinterpret_cast<const float4 *>(box + r4 * 32 + ((uu ^ (r4 & 7)) << 2));
-                        __stcg(reinterpret_cast<float4 *>(dst + static_cast<size_t>(r4) * D + h * 32) + uu, v);
+                        if (r4 < rows)
+                            __stcg(reinterpret_cast<float4 *>(dst + static_cast<size_t>(r4) * D + h * 32) + uu, v);
                     }
                 }
-                p.part_lse[row0 + lane] = m + log2f(l);
+                if (lane < rows)
+                    p.part_lse[row0 + lane] = m + log2f(l);
                 tc_fence_before_sync();
                 continue;
             }
@@ -1051,10 +1054,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
 
-    // Shared prefix: this grid may have started while the suffixes' kernel ran; the merge behind this one
-    // waits for this grid only, so this grid ends after that one.
-    if (kMode == kPrefix && threadIdx.x == 0)
-        asm volatile("griddepcontrol.wait;" ::: "memory");
     tc_fence_before_sync();
     __syncthreads();
     if (warp == kWarpMma) {
@@ -1191,7 +1190,7 @@ cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream, int *encod
     }
 }
 
-PrefixPlan prefix_plan(int B, int Hq, int Hkv, int max_prefix_len, int sm_count)
+PrefixPlan prefix_plan(int B, int Hq, int Hkv, int max_prefix_len, int ctas)
 {
     PrefixPlan pl;
     // A tile holds whole groups of query heads; a group above 128 heads goes in equal parts.
@@ -1204,8 +1203,8 @@ PrefixPlan prefix_plan(int B, int Hq, int Hkv, int max_prefix_len, int sm_count)
     const int tiles = (B + pl.tile_seqs - 1) / pl.tile_seqs;
     pl.tile_pairs = (tiles + 1) / 2;
     pl.lists = static_cast<long long>(Hkv) * sub * pl.tile_pairs;
-    const long long units = pl.lists * ((static_cast<long long>(max_prefix_len) + kBN - 1) / kBN);
-    pl.ctas = static_cast<int>(units < 1 ? 1 : units < sm_count ? units : sm_count);
+    pl.units = pl.lists * ((static_cast<long long>(max_prefix_len) + kBN - 1) / kBN);
+    pl.ctas = static_cast<int>(pl.units < 1 ? 1 : pl.units < ctas ? pl.units : ctas);
     pl.slots = pl.lists + pl.ctas;
     return pl;
 }
@@ -1269,7 +1268,8 @@ cudaError_t launch_prefix(const PrefixArgs &a, cudaStream_t stream, int *encode_
     p.cap = static_cast<int>(cap < a.max_prefix_len ? cap : a.max_prefix_len);
     p.part_o = a.part_o;
     p.part_lse = a.part_lse;
-    return launch_behind(prefill_kernel<D, kPrefix>, pl.ctas, kThreads, C::kSmem, stream, a.behind_suffix, tq, tk, tv, to, p);
+    prefill_kernel<D, kPrefix><<<static_cast<unsigned>(pl.ctas), kThreads, C::kSmem, stream>>>(tq, tk, tv, to, p);
+    return cudaGetLastError();
 }
 
 }  // namespace attn_b200

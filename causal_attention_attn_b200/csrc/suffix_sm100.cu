@@ -108,7 +108,7 @@ template <int kGroups>  // groups of eight query heads in a pair: 1 or 2
 __global__ void __launch_bounds__(32 * kWarps, 1)
     suffix_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const SuffixParams p)
 {
-    asm volatile("griddepcontrol.launch_dependents;");  // the prefix's kernel needs nothing of this one
+    asm volatile("griddepcontrol.launch_dependents;");  // the merge, which waits for this grid's end
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -153,8 +153,16 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
     // Neighbouring ranges go to different SMs, so that few of them still use all.
     const int worker = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
     const int workers = suffix_workers(total, static_cast<int>(gridDim.x));
-    if (worker >= workers)
+    // This grid may have started while the prefix's kernel ran; the merge behind it waits for this one
+    // only, so it ends after that one.
+    auto wait_for_prefix = [&]() {
+        if (lane == 0)
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+    };
+    if (worker >= workers) {
+        wait_for_prefix();
         return;
+    }
     const EvenRange range(total, workers);
     const int g0 = static_cast<int>(range.begin(worker)), n_units = static_cast<int>(range.begin(worker + 1)) - g0;
 
@@ -191,14 +199,14 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
     auto look_up = [&]() {
         const int key = ahead.unit * kKeys, entry = key / p.page_size;
         in_page = key - entry * p.page_size;
-        page = __ldg(p.block_table + static_cast<size_t>(ahead.b) * p.pages_per_seq + entry);
-        if (page < 0 || page >= p.num_pages)
-            page = p.num_pages;  // behind the last page: zeros
+        page = __ldg(p.block_table + static_cast<size_t>(ahead.b) * p.pages_per_seq + entry);  // not waited for here
     };
     auto issue = [&]() {  // lane 0
         const int s = issued % kStages;
         const uint32_t dst = ring + static_cast<uint32_t>(s * kStageBytes), bar = bar0 + 8 * s;
         const int kvh = ahead.pair / p.head_groups;
+        if (page < 0 || page >= p.num_pages)
+            page = p.num_pages;  // behind the last page: zeros
         mbar_arrive_expect_tx(bar, kStageBytes);
         tma_load_4d(dst, &tm_k, bar, 0, in_page, kvh, page);
         tma_load_4d(dst + kBoxBytes, &tm_k, bar, 64, in_page, kvh, page);
@@ -405,6 +413,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
             }
         }
     }
+    wait_for_prefix();
 }
 
 template <int kGroups>
@@ -422,13 +431,12 @@ cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const SuffixPar
             return e;
         attr_set[dev] = true;
     }
-    suffix_kernel<kGroups><<<static_cast<unsigned>(ctas), 32 * kWarps, kSmem, stream>>>(tk, tv, p);
-    return cudaGetLastError();
+    return launch_behind(suffix_kernel<kGroups>, ctas, 32 * kWarps, kSmem, stream, true, tk, tv, p);
 }
 
 }  // namespace
 
-SuffixPlan suffix_plan(int B, int Hq, int Hkv, int max_seq_len, int sm_count)
+SuffixPlan suffix_plan(int B, int Hq, int Hkv, int max_seq_len, int ctas)
 {
     SuffixPlan pl;
     const int group = Hq / Hkv;
@@ -438,7 +446,7 @@ SuffixPlan suffix_plan(int B, int Hq, int Hkv, int max_seq_len, int sm_count)
     // As many CTAs as the workers there can be at most need, so that the others' SMs are free for the
     // prefix's kernel.
     const long long want = (pl.units + kSuffixMinUnits - 1) / kSuffixMinUnits;
-    pl.ctas = static_cast<int>(want < 1 ? 1 : want < sm_count ? want : sm_count);
+    pl.ctas = static_cast<int>(want < 1 ? 1 : want < ctas ? want : ctas);
     pl.piece_floats = static_cast<size_t>(2) * pl.ctas * kWarps * suffix_piece(pl.heads_per_pair);
     return pl;
 }
