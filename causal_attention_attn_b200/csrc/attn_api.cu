@@ -878,8 +878,6 @@ extern "C" int attn_decode_prefix(const void *q, const void *k_pages, const void
         s->prefix_status = static_cast<int *>(word);
     }
     auto at = [&](size_t off) { return static_cast<char *>(workspace) + off; };
-    // The suffixes' kernel needs nothing of the prefix's and starts on the SMs that it leaves free; the
-    // merge waits for both.
     PrefixArgs pa;
     pa.q = q;
     pa.k_pages = k_pages;
@@ -898,14 +896,9 @@ extern "C" int attn_decode_prefix(const void *q, const void *k_pages, const void
     pa.part_o = reinterpret_cast<float *>(at(sp.part_o));
     pa.part_lse = reinterpret_cast<float *>(at(sp.part_lse));
     pa.status = s->prefix_status;
-    int encode_error = 0;
-    if (launch_prefix(pa, stream, &encode_error) != cudaSuccess) {
-        cudaGetLastError();
-        return encode_error ? ATTN_ERR_CUDA : ATTN_ERR_LAUNCH;
-    }
     const bool own = max_seq_len > 0;
+    SuffixArgs a;
     if (own) {
-        SuffixArgs a;
         a.q = q;
         a.k_pages = k_pages;
         a.v_pages = v_pages;
@@ -924,10 +917,11 @@ extern "C" int attn_decode_prefix(const void *q, const void *k_pages, const void
         a.scale = scale;
         a.plan = suffix;
         a.status = s->prefix_status;
-        if (launch_suffix(a, stream, &encode_error) != cudaSuccess) {
-            cudaGetLastError();
-            return encode_error ? ATTN_ERR_CUDA : ATTN_ERR_LAUNCH;
-        }
+    }
+    int encode_error = 0;
+    if (launch_prefix_decode(pa, own ? &a : nullptr, stream, &encode_error) != cudaSuccess) {
+        cudaGetLastError();
+        return encode_error ? ATTN_ERR_CUDA : ATTN_ERR_LAUNCH;
     }
     PrefixMergeArgs m;
     m.plan = pl;

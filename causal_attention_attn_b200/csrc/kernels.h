@@ -190,7 +190,6 @@ struct PrefixArgs {
     float *part_o, *part_lse;
     int *status;
 };
-cudaError_t launch_prefix(const PrefixArgs &a, cudaStream_t stream, int *encode_error);
 
 // The suffixes of a shared-prefix decode (head dim 128, paged bf16 cache): each sequence's token over its
 // own keys. A pair is one (sequence, kv head, up to 16 query heads), its keys are units of 16; all pairs'
@@ -224,8 +223,8 @@ struct SuffixArgs {
     SuffixPlan plan;
     int *status;
 };
-// Launched right behind launch_prefix, which it may overlap.
-cudaError_t launch_suffix(const SuffixArgs &a, cudaStream_t stream, int *encode_error);
+// Prefix and suffixes in one grid: the prefix's blocks first, then (own not null) the suffixes'.
+cudaError_t launch_prefix_decode(const PrefixArgs &a, const SuffixArgs *own, cudaStream_t stream, int *encode_error);
 
 // Joins the prefix's segments and the suffixes' results into o (bf16) and lse (natural log).
 struct PrefixMergeArgs {

@@ -59,6 +59,7 @@
 
 #include "kernels.h"
 #include "sm100_ptx.cuh"
+#include "suffix_sm100.cuh"
 #include "tma_host.h"
 
 namespace attn_b200 {
@@ -149,6 +150,7 @@ struct Params {
     int tile_pairs = 0; // pairs of tiles per head: heads * tile_pairs lists of KV tiles
     float *part_o = nullptr;    // [segment slot][256][128]
     float *part_lse = nullptr;  // [segment slot][256], log2 units
+    int ctas = 0;               // blocks that work on the prefix, the grid's first
 };
 
 // What an instantiation of the kernel computes: attention over a dense cache, over a paged,
@@ -276,7 +278,7 @@ __device__ __forceinline__ Segments find_segments(const Params &p)
     sg.len = prefix_length(p);
     sg.tiles = (sg.len + kBN - 1) / kBN;
     const uint32_t total = static_cast<uint32_t>(p.heads) * p.tile_pairs * sg.tiles;
-    const EvenRange r(total, gridDim.x);
+    const EvenRange r(total, static_cast<uint32_t>(p.ctas));
     sg.begin = static_cast<int>(r.begin(blockIdx.x));
     sg.end = static_cast<int>(r.begin(blockIdx.x + 1));
     sg.first_list = sg.tiles ? sg.begin / sg.tiles : 0;
@@ -379,14 +381,12 @@ __device__ __forceinline__ int next_active(const Params &p, int r)
 }
 
 template <int D, int kMode>
-__global__ void __launch_bounds__(kThreads, 1)
-    prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o, const Params p)
+__device__ __forceinline__ void run_tiles(const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
+                                          const CUtensorMap &tm_o, const Params &p, uint8_t *smem_raw)
 {
     using C = Cfg<D>;
     constexpr bool kPaged = kMode == kPagedCache;  // per-sequence lengths; rows may see no key
     constexpr bool kPages = kMode != kDense;       // K and V in pages
-    extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t s_base = smem_u32(smem);
     const uint32_t sQ = s_base + C::kOffQ;
@@ -447,7 +447,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         if (warp == 11 && lane == 0)
             s_segments = find_segments(p);
-        asm volatile("griddepcontrol.launch_dependents;");  // the suffixes' kernel: it needs nothing of this one
     }
     if (warp == kWarpTma && lane == 0) {
         tma_prefetch_desc(&tm_q);
@@ -1063,30 +1062,54 @@ __global__ void __launch_bounds__(kThreads, 1)
 #undef BAR
 }
 
-// Sets an instantiation's attributes on the current device once.
 template <int D, int kMode>
-cudaError_t prepare()
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o, const Params p)
 {
-    using C = Cfg<D>;
-    // Per device: the attribute applies to the device current when it is set (benign race between
-    // host threads: every caller sets the same value).
-    static bool attr_set[kMaxDevices] = {};
+    extern __shared__ uint8_t smem_raw[];
+    run_tiles<D, kMode>(tm_q, tm_k, tm_v, tm_o, p, smem_raw);
+}
+
+// Decode over a shared prefix: the first p.ctas blocks take the prefix, the rest the suffixes. One launch,
+// because neither needs the other, and the merge behind it then waits for one grid.
+template <int kGroups>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefix_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                         const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_sk,
+                         const __grid_constant__ CUtensorMap tm_sv, const Params p, const suffix::SuffixParams sp)
+{
+    static_assert(kThreads == 32 * kSuffixWarps, "one block size");
+    extern __shared__ uint8_t smem_raw[];
+    asm volatile("griddepcontrol.launch_dependents;");  // the merge, which waits for this grid's end
+    if (static_cast<int>(blockIdx.x) < p.ctas)
+        run_tiles<128, kPrefix>(tm_q, tm_k, tm_v, tm_q, p, smem_raw);
+    else
+        suffix::run<kGroups>(tm_sk, tm_sv, sp, smem_raw, static_cast<int>(blockIdx.x) - p.ctas,
+                             static_cast<int>(gridDim.x) - p.ctas);
+}
+
+// Sets a kernel's attributes on the current device once (`set`: its flags, by device; benign race
+// between host threads: every caller sets the same value).
+template <typename Kernel>
+cudaError_t prepare(Kernel kernel, int smem, bool (&set)[kMaxDevices])
+{
     const int dev = current_device_index();
     if (dev < 0)
         return cudaErrorInvalidDevice;
-    if (attr_set[dev])
+    if (set[dev])
         return cudaSuccess;
     // The setmaxnreg split inside the kernel is only valid for the register count it was
     // written for; refuse to launch a build that was compiled to anything else.
     cudaFuncAttributes fa;
-    cudaError_t e = cudaFuncGetAttributes(&fa, prefill_kernel<D, kMode>);
+    cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
     if (e != cudaSuccess)
         return e;
     if (fa.numRegs != kLaunchRegs)
         return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(prefill_kernel<D, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess)
-        attr_set[dev] = true;
+        set[dev] = true;
     return e;
 }
 
@@ -1129,7 +1152,8 @@ cudaError_t launch(const PrefillArgs &a, cudaStream_t stream, int *encode_error)
             return cudaErrorInvalidValue;
     }
 
-    const cudaError_t ready = prepare<D, kMode>();
+    static bool set[kMaxDevices] = {};
+    const cudaError_t ready = prepare(prefill_kernel<D, kMode>, C::kSmem, set);
     if (ready != cudaSuccess)
         return ready;
     Params p;
@@ -1209,7 +1233,22 @@ PrefixPlan prefix_plan(int B, int Hq, int Hkv, int max_prefix_len, int ctas)
     return pl;
 }
 
-cudaError_t launch_prefix(const PrefixArgs &a, cudaStream_t stream, int *encode_error)
+SuffixPlan suffix_plan(int B, int Hq, int Hkv, int max_seq_len, int ctas)
+{
+    SuffixPlan pl;
+    const int group = Hq / Hkv;
+    pl.heads_per_pair = group < 16 ? group : 16;
+    pl.head_groups = (group + 15) / 16;
+    pl.units = static_cast<long long>(B) * Hkv * pl.head_groups * ((static_cast<long long>(max_seq_len) + kSuffixUnitKeys - 1) / kSuffixUnitKeys);
+    // As many CTAs as the workers there can be at most need, so that the others' SMs are free for the
+    // prefix.
+    const long long want = (pl.units + kSuffixMinUnits - 1) / kSuffixMinUnits;
+    pl.ctas = static_cast<int>(want < 1 ? 1 : want < ctas ? want : ctas);
+    pl.piece_floats = static_cast<size_t>(2) * pl.ctas * kSuffixWarps * suffix_piece(pl.heads_per_pair);
+    return pl;
+}
+
+cudaError_t launch_prefix_decode(const PrefixArgs &a, const SuffixArgs *own, cudaStream_t stream, int *encode_error)
 {
     constexpr int D = 128;
     using C = Cfg<D>;
@@ -1220,7 +1259,7 @@ cudaError_t launch_prefix(const PrefixArgs &a, cudaStream_t stream, int *encode_
         return cudaErrorInitializationError;
     }
     const PrefixPlan &pl = a.plan;
-    CUtensorMap tq, tk, tv, to;
+    CUtensorMap tq, tk, tv, tsk, tsv;
     // q as (dim, head of the group, sequence, kv head): boxes of 64 dims, a group, tile_seqs sequences.
     {
         const cuuint64_t dims[4] = {D, static_cast<cuuint64_t>(pl.group), static_cast<cuuint64_t>(a.B),
@@ -1243,10 +1282,14 @@ cudaError_t launch_prefix(const PrefixArgs &a, cudaStream_t stream, int *encode_
         !make_map4(encode, &tv, a.v_pages, 2, D, a.page_size, a.Hkv, a.num_pages, pst, 64, rows, CU_TENSOR_MAP_SWIZZLE_128B,
                    encode_error))
         return cudaErrorInvalidValue;
-    to = tq;  // unused: the partials leave by plain stores
-    const cudaError_t ready = prepare<D, kPrefix>();
-    if (ready != cudaSuccess)
-        return ready;
+    suffix::SuffixParams sp{};
+    if (own) {
+        if (!suffix::make_maps(encode, *own, &tsk, &tsv, encode_error))
+            return cudaErrorInvalidValue;
+        sp = suffix::params(*own);
+    } else {
+        tsk = tsv = tk;  // no block reads them
+    }
     Params p{};
     p.status = a.status;
     p.B = a.B;
@@ -1268,8 +1311,17 @@ cudaError_t launch_prefix(const PrefixArgs &a, cudaStream_t stream, int *encode_
     p.cap = static_cast<int>(cap < a.max_prefix_len ? cap : a.max_prefix_len);
     p.part_o = a.part_o;
     p.part_lse = a.part_lse;
-    prefill_kernel<D, kPrefix><<<static_cast<unsigned>(pl.ctas), kThreads, C::kSmem, stream>>>(tq, tk, tv, to, p);
-    return cudaGetLastError();
+    p.ctas = pl.ctas;
+    constexpr int kSmem = C::kSmem > suffix::kSmem ? C::kSmem : suffix::kSmem;
+    static bool set[2][kMaxDevices] = {};
+    auto launch = [&](auto kernel, bool (&done)[kMaxDevices]) {
+        const cudaError_t ready = prepare(kernel, kSmem, done);
+        if (ready != cudaSuccess)
+            return ready;
+        kernel<<<static_cast<unsigned>(pl.ctas + (own ? own->plan.ctas : 0)), kThreads, kSmem, stream>>>(tq, tk, tv, tsk, tsv, p, sp);
+        return cudaGetLastError();
+    };
+    return own && own->plan.heads_per_pair > 8 ? launch(prefix_decode_kernel<2>, set[1]) : launch(prefix_decode_kernel<1>, set[0]);
 }
 
 }  // namespace attn_b200

@@ -1,5 +1,5 @@
 /*
- * suffix_sm100.cu — the suffixes of a shared-prefix decode (attn_decode_prefix): one new token per
+ * suffix_sm100.cuh — the suffixes of a shared-prefix decode (attn_decode_prefix): one new token per
  * sequence over the sequence's own keys in a paged bf16 cache, head dim 128, results in fp32 for the
  * merge with the prefix (merge_sm100.cu).
  *
@@ -24,6 +24,8 @@
  * A warp that holds a whole pair writes its result; pieces of pairs that several warps share go to the
  * workspace and the merge reads them there.
  */
+#pragma once
+
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -36,7 +38,7 @@
 #include "tma_host.h"
 
 namespace attn_b200 {
-namespace {
+namespace suffix {
 
 constexpr int kD = 128;
 constexpr int kKeys = kSuffixUnitKeys;  // keys of a unit
@@ -104,12 +106,12 @@ struct Cursor {
     int b, pair, unit, units;
 };
 
-template <int kGroups>  // groups of eight query heads in a pair: 1 or 2
-__global__ void __launch_bounds__(32 * kWarps, 1)
-    suffix_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const SuffixParams p)
+// The block's 32 kWarps threads; `cta` of `ctas` blocks that do this. kGroups: groups of eight query
+// heads in a pair, 1 or 2.
+template <int kGroups>
+__device__ __forceinline__ void run(const CUtensorMap &tm_k, const CUtensorMap &tm_v, const SuffixParams &p, uint8_t *smem_raw,
+                                    int cta, int ctas)
 {
-    asm volatile("griddepcontrol.launch_dependents;");  // the merge, which waits for this grid's end
-    extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffMisc);
@@ -151,18 +153,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
     __syncthreads();
     const int total = start[p.B];
     // Neighbouring ranges go to different SMs, so that few of them still use all.
-    const int worker = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
-    const int workers = suffix_workers(total, static_cast<int>(gridDim.x));
-    // This grid may have started while the prefix's kernel ran; the merge behind it waits for this one
-    // only, so it ends after that one.
-    auto wait_for_prefix = [&]() {
-        if (lane == 0)
-            asm volatile("griddepcontrol.wait;" ::: "memory");
-    };
-    if (worker >= workers) {
-        wait_for_prefix();
+    const int worker = warp * ctas + cta;
+    const int workers = suffix_workers(total, ctas);
+    if (worker >= workers)
         return;
-    }
     const EvenRange range(total, workers);
     const int g0 = static_cast<int>(range.begin(worker)), n_units = static_cast<int>(range.begin(worker + 1)) - g0;
 
@@ -413,60 +407,18 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
             }
         }
     }
-    wait_for_prefix();
 }
 
-template <int kGroups>
-cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const SuffixParams &p, int ctas, cudaStream_t stream)
+// Pages [num_pages][Hkv][page_size][D] as (dim, slot, kv head, page): boxes of 64 dims, 16 keys.
+inline bool make_maps(PFN_cuTensorMapEncodeTiled_v12000 encode, const SuffixArgs &a, CUtensorMap *tk, CUtensorMap *tv, int *err)
 {
-    // Per device: the attribute applies to the device current when it is set.
-    static bool attr_set[kMaxDevices] = {};
-    const int dev = current_device_index();
-    if (dev < 0)
-        return cudaErrorInvalidDevice;
-    if (!attr_set[dev]) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(suffix_kernel<kGroups>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-        if (e != cudaSuccess)
-            return e;
-        attr_set[dev] = true;
-    }
-    return launch_behind(suffix_kernel<kGroups>, ctas, 32 * kWarps, kSmem, stream, true, tk, tv, p);
-}
-
-}  // namespace
-
-SuffixPlan suffix_plan(int B, int Hq, int Hkv, int max_seq_len, int ctas)
-{
-    SuffixPlan pl;
-    const int group = Hq / Hkv;
-    pl.heads_per_pair = group < 16 ? group : 16;
-    pl.head_groups = (group + 15) / 16;
-    pl.units = static_cast<long long>(B) * Hkv * pl.head_groups * ((static_cast<long long>(max_seq_len) + kKeys - 1) / kKeys);
-    // As many CTAs as the workers there can be at most need, so that the others' SMs are free for the
-    // prefix's kernel.
-    const long long want = (pl.units + kSuffixMinUnits - 1) / kSuffixMinUnits;
-    pl.ctas = static_cast<int>(want < 1 ? 1 : want < ctas ? want : ctas);
-    pl.piece_floats = static_cast<size_t>(2) * pl.ctas * kWarps * suffix_piece(pl.heads_per_pair);
-    return pl;
-}
-
-cudaError_t launch_suffix(const SuffixArgs &a, cudaStream_t stream, int *encode_error)
-{
-    *encode_error = 0;
-    auto encode = get_encode_fn();
-    if (!encode) {
-        *encode_error = -1;
-        return cudaErrorInitializationError;
-    }
-    // Pages [num_pages][Hkv][page_size][D] as (dim, slot, kv head, page): boxes of 64 dims, 16 keys.
-    CUtensorMap tk, tv;
     const Strides st{static_cast<long long>(a.Hkv) * a.page_size * kD, static_cast<long long>(a.page_size) * kD, kD};
-    if (!make_map4(encode, &tk, a.k_pages, 2, kD, a.page_size, a.Hkv, a.num_pages, st, 64, kKeys, CU_TENSOR_MAP_SWIZZLE_128B,
-                   encode_error) ||
-        !make_map4(encode, &tv, a.v_pages, 2, kD, a.page_size, a.Hkv, a.num_pages, st, 64, kKeys, CU_TENSOR_MAP_SWIZZLE_128B,
-                   encode_error))
-        return cudaErrorInvalidValue;
+    return make_map4(encode, tk, a.k_pages, 2, kD, a.page_size, a.Hkv, a.num_pages, st, 64, kKeys, CU_TENSOR_MAP_SWIZZLE_128B, err) &&
+           make_map4(encode, tv, a.v_pages, 2, kD, a.page_size, a.Hkv, a.num_pages, st, 64, kKeys, CU_TENSOR_MAP_SWIZZLE_128B, err);
+}
+
+inline SuffixParams params(const SuffixArgs &a)
+{
     SuffixParams p;
     p.q = static_cast<const __nv_bfloat16 *>(a.q);
     p.seq_lens = a.seq_lens;
@@ -486,7 +438,8 @@ cudaError_t launch_suffix(const SuffixArgs &a, cudaStream_t stream, int *encode_
     p.pages_per_seq = a.pages_per_seq;
     p.cap = a.cap;
     p.scale_log2 = a.scale * 1.4426950408889634f;
-    return a.plan.heads_per_pair <= 8 ? launch<1>(tk, tv, p, a.plan.ctas, stream) : launch<2>(tk, tv, p, a.plan.ctas, stream);
+    return p;
 }
 
+}  // namespace suffix
 }  // namespace attn_b200
