@@ -742,8 +742,11 @@ struct PrefixSpace {
     size_t pieces, o_suffix, lse_suffix, part_o, part_lse, bytes;  // byte offsets
 };
 
-PrefixSpace prefix_space(int B, int Hq, const PrefixPlan &pl, const SuffixPlan &suffix)
+// Sized for as many CTAs as the device has SMs, whatever the plan takes of them, so that a workspace for
+// larger batches and lengths serves smaller ones.
+PrefixSpace prefix_space(int B, int Hq, const PrefixPlan &pl, const SuffixPlan &suffix, int sm_count)
 {
+    const size_t slots = static_cast<size_t>(pl.lists) + sm_count;
     size_t at = 0;
     auto take = [&](size_t n) {
         const size_t here = at;
@@ -752,11 +755,11 @@ PrefixSpace prefix_space(int B, int Hq, const PrefixPlan &pl, const SuffixPlan &
     };
     PrefixSpace sp;
     const size_t rows = static_cast<size_t>(B) * Hq;
-    sp.pieces = take(suffix.piece_floats * sizeof(float));
+    sp.pieces = take(sizeof(float) * 2 * sm_count * kSuffixWarps * suffix_piece(suffix.heads_per_pair));
     sp.o_suffix = take(rows * 128 * sizeof(float));
     sp.lse_suffix = take(rows * sizeof(float));
-    sp.part_o = take(static_cast<size_t>(pl.slots) * 256 * 128 * sizeof(float));
-    sp.part_lse = take(static_cast<size_t>(pl.slots) * 256 * sizeof(float));
+    sp.part_o = take(slots * 256 * 128 * sizeof(float));
+    sp.part_lse = take(slots * 256 * sizeof(float));
     sp.bytes = at;
     return sp;
 }
@@ -767,7 +770,7 @@ int check_prefix_sizes(int B, int Hq, int Hkv, int max_prefix_len, int max_seq_l
         return ATTN_ERR_SHAPE;
     if (Hq % Hkv != 0)
         return ATTN_ERR_GQA;
-    // A kv head's tiles hold at least one row of each sequence: slots * 256 rows stay below 2^31.
+    // Rows of the partials (256 for each list and CTA) stay far below 2^31.
     if (static_cast<long long>(B) * Hq > (1LL << 22))
         return ATTN_ERR_SHAPE;
     return ATTN_OK;
@@ -780,26 +783,28 @@ int plan_prefix(const DeviceState &s, int B, int Hq, int Hkv, int max_prefix_len
     *pl = prefix_plan(B, Hq, Hkv, max_prefix_len, s.sm_count);
     *suffix = suffix_plan(B, Hq, Hkv, max_seq_len, s.sm_count);
     if (max_seq_len > 0 && max_prefix_len > 0) {
-        // Side by side where that costs the prefix little: with n KV tiles to a CTA it needs ceil(units /
-        // n) SMs, and the rest take the suffixes if they are done with them before. Measured: the prefix's
-        // kernel takes 4.5 us and 1.6 us a KV tile (2.0 with two query tiles), the suffixes' 3.4 us and
-        // 0.112 us for each unit of an SM (8 KB at 73 GB/s); in turn the suffixes cost 4 us at the least, so
-        // the prefix may lose that much. Both lengths are bounds here: a shorter suffix leaves SMs idle
-        // that the prefix did without.
-        const long long n0 = (pl->units + s.sm_count - 1) / s.sm_count;
-        const double tile_us = pl->tile_pairs * pl->tile_seqs >= B ? 1.6 : 2.0;
-        for (long long n = n0; tile_us * static_cast<double>(n - n0) < 4.0; ++n) {
-            const int ctas = static_cast<int>((pl->units + n - 1) / n), rest = s.sm_count - ctas;
-            if (rest < 1 || 3.4 + 0.112 * static_cast<double>(suffix->units) / rest > 4.5 + tile_us * static_cast<double>(n))
+        // Side by side where that costs the prefix little: the fewer CTAs it takes, the more SMs are left
+        // for the suffixes, if they are done there before it is. Measured: the suffixes take 3.4 us and
+        // 0.112 us for each unit of an SM (8 KB at 73 GB/s); in turn they cost 4 us at the least, so the
+        // prefix may lose that much. Both lengths are bounds here: a shorter suffix leaves SMs idle that the
+        // prefix did without.
+        const double least = pl->us;
+        auto suffix_us = [&](int sms) { return 3.4 + 0.112 * static_cast<double>(suffix->units) / sms; };
+        for (const double loss : {0.0, 2.0, 4.0}) {
+            const double need = std::ceil(0.112 * static_cast<double>(suffix->units) / (least + loss - 3.4));
+            if (need >= s.sm_count)
                 continue;
-            *pl = prefix_plan(B, Hq, Hkv, max_prefix_len, ctas);
+            const PrefixPlan fewer =
+                prefix_plan(B, Hq, Hkv, max_prefix_len, s.sm_count - std::max(1, static_cast<int>(need)));
+            const int rest = s.sm_count - fewer.ctas;
+            if (fewer.us > least + 4.0 || suffix_us(rest) > fewer.us)
+                continue;
+            *pl = fewer;
             *suffix = suffix_plan(B, Hq, Hkv, max_seq_len, rest);
             break;
         }
     }
-    if (pl->slots * 256 > INT_MAX)
-        return ATTN_ERR_SHAPE;
-    *sp = prefix_space(B, Hq, *pl, *suffix);
+    *sp = prefix_space(B, Hq, *pl, *suffix, s.sm_count);
     return ATTN_OK;
 }
 

@@ -169,15 +169,21 @@ cudaError_t launch_prefill_fp8(const PrefillFp8Args &a, cudaStream_t stream, int
 
 // The shared-prefix part of a decode over paged caches (head dim 128): B sequences, one new token each,
 // over the prefix's keys. The packed rows of one kv head make tiles of 128, two tiles share a list of KV
-// tiles, and the lists are cut evenly over `ctas` CTAs; every (list, CTA) segment leaves fp32 partials
+// tiles, and the lists are cut over `ctas` CTAs; every (list, CTA) segment leaves fp32 partials
 // in slot list + CTA: part_o [slots][2][128][128] normalised, part_lse [slots][2][128] in log2 units.
 struct PrefixPlan {
     int group, sub_groups;  // query heads of a row tile's group; parts of a group above 128 heads
     int tile_seqs;          // sequences in a tile
     int tile_pairs;         // per head
-    long long lists, slots;
+    long long lists;
     long long units;        // KV tiles of all lists, at most
     int ctas;
+    // CTAs of each list, and of each head's last list (which may hold one tile only and then needs fewer);
+    // no range crosses from one list to the next. per_last 0: all lists, laid end to end, are cut into
+    // `ctas` ranges.
+    int per_list, per_last;
+    __host__ __device__ int per_head() const { return (tile_pairs - 1) * per_list + per_last; }
+    double us;              // what the kernel is expected to take
 };
 // `ctas`: the most to launch.
 PrefixPlan prefix_plan(int B, int Hq, int Hkv, int max_prefix_len, int ctas);
@@ -211,7 +217,6 @@ struct SuffixPlan {
     int heads_per_pair, head_groups;
     long long units;  // at most: the lengths are read on the device
     int ctas;
-    size_t piece_floats;
 };
 SuffixPlan suffix_plan(int B, int Hq, int Hkv, int max_seq_len, int ctas);
 struct SuffixArgs {

@@ -127,7 +127,11 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const Pr
     const int list = part_of_heads * a.plan.tile_pairs + tile / 2;
     const int tiles = (min(max(__ldg(a.prefix_len), 0), a.cap) + kTile - 1) / kTile;
     int c0 = 0, n_prefix = 0;
-    if (tiles > 0) {
+    if (a.plan.per_last > 0) {
+        const int pair = tile / 2;
+        c0 = part_of_heads * a.plan.per_head() + pair * a.plan.per_list;
+        n_prefix = min(pair + 1 == a.plan.tile_pairs ? a.plan.per_last : a.plan.per_list, tiles);
+    } else if (tiles > 0) {
         const EvenRange range(static_cast<unsigned>(a.plan.lists) * tiles, a.by_ctas);
         c0 = static_cast<int>(range.part_of(list * tiles));
         n_prefix = static_cast<int>(range.part_of((list + 1) * tiles - 1)) - c0 + 1;
@@ -165,32 +169,44 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const Pr
     }
     const int n = n_prefix + n_suffix;
 
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-
-    // Part k: its O row and its LSE; -inf behind the last.
-    auto part = [&](int k, const float **o) -> float {
-        *o = a.part_o;
+    // Where part k's O row and its LSE lie; null behind the last.
+    auto find_part = [&](int k, const float **o, const float **lse) {
+        *o = *lse = nullptr;
         if (k < n_prefix) {
             const long long r = (static_cast<long long>(list + c0 + k) * 2 + (tile & 1)) * kTile + in_tile;
             *o = a.part_o + r * D;
-            return __ldcg(a.part_lse + r);
-        }
-        if (k >= n)
-            return -INFINITY;
-        if (n_suffix == 1) {  // the whole pair
+            *lse = a.part_lse + r;
+        } else if (k < n && n_suffix == 1) {  // the whole pair
             *o = a.o_suffix + static_cast<size_t>(row) * D;
-            return __ldcg(a.lse_suffix + row);
+            *lse = a.lse_suffix + row;
+        } else if (k < n) {
+            const int i = k - n_prefix, per = a.suffix.heads_per_pair;
+            const float *piece = a.pieces + (static_cast<size_t>(s0 + i) * 2 + (i == 0 ? first_piece : 0)) * suffix_piece(per);
+            *o = piece + in_pair * D;
+            *lse = piece + per * D + in_pair;
         }
-        const int i = k - n_prefix, per = a.suffix.heads_per_pair;
-        const float *piece = a.pieces + (static_cast<size_t>(s0 + i) * 2 + (i == 0 ? first_piece : 0)) * suffix_piece(per);
-        *o = piece + in_pair * D;
-        return __ldcg(piece + per * D + in_pair);
     };
+    const float *o, *lse;
+    find_part(lane * kSplit + warp, &o, &lse);
     float M = -INFINITY, W = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int k = 0; k < n; k += 32 * kSplit) {
-        const float *o;
-        const float l = part(k + lane * kSplit + warp, &o);
+        if (k > 0)
+            find_part(k + lane * kSplit + warp, &o, &lse);
+        const float l = lse ? __ldcg(lse) : -INFINITY;
+        const int parts = min(32, (n - k - warp + kSplit - 1) / kSplit);
+        // Eight parts' rows at a time, the first eight sent for before their weights are known.
+        float4 v[8];
+        auto fetch = [&](int t) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float *po = reinterpret_cast<const float *>(
+                    __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), min(t + j, 31)));
+                v[j] = t + j < parts ? __ldcg(reinterpret_cast<const float4 *>(po) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        };
+        fetch(0);
         float m = l;
 #pragma unroll
         for (int s = 16; s > 0; s >>= 1)
@@ -202,28 +218,19 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const Pr
         M = new_m;
         // fmaxf drops NaN: a part with a NaN LSE (from NaN scores) keeps a NaN weight.
         const float w = l == -INFINITY ? 0.f : exp2f(l - M);
-        const int parts = min(32, (n - k - warp + kSplit - 1) / kSplit);
         for (int t = 0; t < parts; t += 8) {
-            float4 v[8];
-            float wt[8];
+            if (t > 0)
+                fetch(t);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int from = min(t + j, 31);
-                wt[j] = __shfl_sync(0xffffffffu, w, from);
-                const float *po = reinterpret_cast<const float *>(
-                    __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), from));
-                v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (t + j < parts && wt[j] != 0.f)
-                    v[j] = __ldcg(reinterpret_cast<const float4 *>(po) + lane);
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float u = t + j < parts ? wt[j] : 0.f;
-                acc.x = fmaf(u, v[j].x, acc.x);
-                acc.y = fmaf(u, v[j].y, acc.y);
-                acc.z = fmaf(u, v[j].z, acc.z);
-                acc.w = fmaf(u, v[j].w, acc.w);
-                W += u;
+                const float wt = __shfl_sync(0xffffffffu, w, min(t + j, 31)), u = t + j < parts ? wt : 0.f;
+                if (u != 0.f) {  // a part of weight 0 may hold anything (all its scores -inf)
+                    acc.x = fmaf(u, v[j].x, acc.x);
+                    acc.y = fmaf(u, v[j].y, acc.y);
+                    acc.z = fmaf(u, v[j].z, acc.z);
+                    acc.w = fmaf(u, v[j].w, acc.w);
+                    W += u;
+                }
             }
         }
     }

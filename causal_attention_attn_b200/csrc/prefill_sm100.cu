@@ -53,6 +53,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <mutex>
@@ -151,6 +152,7 @@ struct Params {
     float *part_o = nullptr;    // [segment slot][256][128]
     float *part_lse = nullptr;  // [segment slot][256], log2 units
     int ctas = 0;               // blocks that work on the prefix, the grid's first
+    int per_list = 0, per_last = 0;  // of them for each list (PrefixPlan)
 };
 
 // What an instantiation of the kernel computes: attention over a dense cache, over a paged,
@@ -169,6 +171,18 @@ __device__ __forceinline__ void tma_store_4d(const CUtensorMap *map, uint32_t sr
     asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];"
                  ::"l"(reinterpret_cast<uint64_t>(map)), "r"(src), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
                  : "memory");
+}
+
+__device__ __forceinline__ void st_shared4(uint32_t addr, float4 v)
+{
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+
+__device__ __forceinline__ float4 ld_shared4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
 }
 
 // Reference max of a row that has seen no key yet (paged variant): finite, so that the weights of
@@ -255,9 +269,9 @@ struct Item {
 };
 
 // ---- shared prefix of a decode ------------------------------------------------------------------
-// For each head and pair of tiles there is a list of all KV tiles of the prefix; the lists, laid end
-// to end, are cut into one range per CTA (even_range: lengths differ by one at most), so that a few rows
-// still use every SM. A CTA's part of one list is a segment: an item whose unnormalised softmax is
+// For each head and pair of tiles there is a list of all KV tiles of the prefix. The lists are cut into
+// ranges, one per CTA, whose lengths differ by one at most (EvenRange), so that a few rows still use every
+// SM: each list by itself, or all of them laid end to end (PrefixPlan says which). A CTA's part of one list is a segment: an item whose unnormalised softmax is
 // finished here and whose rows are merged with the list's other segments, and with the sequences' own
 // keys, by prefix_merge_kernel. Segment (list, CTA) has slot list + CTA: both grow along the lists, and
 // one of them does from each segment to the next, so slots are distinct and below lists + CTAs.
@@ -277,11 +291,23 @@ __device__ __forceinline__ Segments find_segments(const Params &p)
     Segments sg;
     sg.len = prefix_length(p);
     sg.tiles = (sg.len + kBN - 1) / kBN;
-    const uint32_t total = static_cast<uint32_t>(p.heads) * p.tile_pairs * sg.tiles;
-    const EvenRange r(total, static_cast<uint32_t>(p.ctas));
-    sg.begin = static_cast<int>(r.begin(blockIdx.x));
-    sg.end = static_cast<int>(r.begin(blockIdx.x + 1));
-    sg.first_list = sg.tiles ? sg.begin / sg.tiles : 0;
+    if (p.per_last > 0) {
+        const int per_head = (p.tile_pairs - 1) * p.per_list + p.per_last;
+        const int head = static_cast<int>(blockIdx.x) / per_head;
+        int i = static_cast<int>(blockIdx.x) - head * per_head;
+        const int pair = p.tile_pairs > 1 ? min(i / p.per_list, p.tile_pairs - 1) : 0;
+        i -= pair * p.per_list;
+        const int list = head * p.tile_pairs + pair;
+        const EvenRange r(sg.tiles, pair + 1 == p.tile_pairs ? p.per_last : p.per_list);
+        sg.begin = list * sg.tiles + static_cast<int>(r.begin(i));
+        sg.end = list * sg.tiles + static_cast<int>(r.begin(i + 1));
+        sg.first_list = list;
+    } else {
+        const EvenRange r(static_cast<uint32_t>(p.heads) * p.tile_pairs * sg.tiles, static_cast<uint32_t>(p.ctas));
+        sg.begin = static_cast<int>(r.begin(blockIdx.x));
+        sg.end = static_cast<int>(r.begin(blockIdx.x + 1));
+        sg.first_list = sg.tiles ? sg.begin / sg.tiles : 0;
+    }
     return sg;
 }
 
@@ -958,29 +984,30 @@ __device__ __forceinline__ void run_tiles(const CUtensorMap &tm_q, const CUtenso
                 // units XOR row % 8) so that eight lanes store one row's 128 bytes, and the LSE in log2
                 // units. (TMA stores from the box, waiting for each to be read, took 1.9 us a tile.)
                 // Only rows of sequences: an SM stores 32 bytes a cycle, so a full tile's 64 KB take a good us.
-                float *box = reinterpret_cast<float *>(smem + C::kOffStage + warp * C::kWarpStageBytes);
+                const uint32_t box = s_base + C::kOffStage + static_cast<uint32_t>(warp * C::kWarpStageBytes);
                 const int row0 = (cur.slot * 2 + x) * kBM + 32 * (warp & 3);
-                float *dst = p.part_o + static_cast<size_t>(row0) * D;
                 const int rr = lane >> 3, uu = lane & 7;
+                float *dst = p.part_o + static_cast<size_t>(row0 + rr) * D + 4 * uu;
                 const int rows = min(p.tile_seqs, p.B - q0) * p.group - 32 * (warp & 3);  // of this warp's 32
-#pragma unroll 1  // once a segment: less code to fetch counts for more
-                for (int h = 0; h < (rows > 0 ? D / 32 : 0); ++h) {
+#pragma unroll 1  // once a segment: less code to fetch counts for more (unrolled it took 0.5 us longer)
+                for (int h = 0; h < (rows > 0 ? D / 32 : 0); ++h, dst += 32) {
                     uint32_t ov[32];
                     tmem_ld32_wait(tO + h * 32, ov);
                     __syncwarp();  // the rows of the 32 dims before are read
 #pragma unroll
                     for (int u = 0; u < 8; ++u)
-                        *reinterpret_cast<float4 *>(box + lane * 32 + ((u ^ (lane & 7)) << 2)) =
-                            make_float4(__uint_as_float(ov[4 * u]) * inv_l, __uint_as_float(ov[4 * u + 1]) * inv_l,
-                                        __uint_as_float(ov[4 * u + 2]) * inv_l, __uint_as_float(ov[4 * u + 3]) * inv_l);
+                        st_shared4(box + static_cast<uint32_t>(lane * 128 + ((u ^ (lane & 7)) << 4)),
+                                   make_float4(__uint_as_float(ov[4 * u]) * inv_l, __uint_as_float(ov[4 * u + 1]) * inv_l,
+                                               __uint_as_float(ov[4 * u + 2]) * inv_l, __uint_as_float(ov[4 * u + 3]) * inv_l));
                     __syncwarp();
+                    float4 v[8];
 #pragma unroll
-                    for (int t = 0; t < 8; ++t) {
-                        const int r4 = 4 * t + rr;
-                        const float4 v = *reinterpret_cast<const float4 *>(box + r4 * 32 + ((uu ^ (r4 & 7)) << 2));
-                        if (r4 < rows)
-                            __stcg(reinterpret_cast<float4 *>(dst + static_cast<size_t>(r4) * D + h * 32) + uu, v);
-                    }
+                    for (int t = 0; t < 8; ++t)
+                        v[t] = ld_shared4(box + static_cast<uint32_t>((4 * t + rr) * 128 + ((uu ^ ((4 * t + rr) & 7)) << 4)));
+#pragma unroll
+                    for (int t = 0; t < 8; ++t)
+                        if (4 * t + rr < rows)
+                            __stcg(reinterpret_cast<float4 *>(dst + 4 * t * D), v[t]);
                 }
                 if (lane < rows)
                     p.part_lse[row0 + lane] = m + log2f(l);
@@ -1228,8 +1255,30 @@ PrefixPlan prefix_plan(int B, int Hq, int Hkv, int max_prefix_len, int ctas)
     pl.tile_pairs = (tiles + 1) / 2;
     pl.lists = static_cast<long long>(Hkv) * sub * pl.tile_pairs;
     pl.units = pl.lists * ((static_cast<long long>(max_prefix_len) + kBN - 1) / kBN);
+    // A KV tile takes 2.0 us of an SM, 1.6 us in a list of one query tile; a segment's start and end 4.5 us
+    // for the first of a CTA and 2 us for another. Cutting each list by itself gives every CTA one segment
+    // but may leave SMs without work; cutting all lists as one gives most CTAs two. Whichever ends first.
+    const long long tiles_kv = (static_cast<long long>(max_prefix_len) + kBN - 1) / kBN;
+    const double full_us = 2.0, last_us = tiles % 2 ? 1.6 : 2.0;
+    auto up = [](long long n, long long d) { return (n + d - 1) / d; };
+    pl.per_list = pl.per_last = 0;
     pl.ctas = static_cast<int>(pl.units < 1 ? 1 : pl.units < ctas ? pl.units : ctas);
-    pl.slots = pl.lists + pl.ctas;
+    pl.us = 4.5 + full_us * static_cast<double>(up(pl.units, pl.ctas)) + 2.0;
+    const long long heads = static_cast<long long>(Hkv) * sub, each = ctas / heads;  // CTAs for one head
+    for (long long per = pl.tile_pairs > 1 ? 1 : 0; tiles_kv > 0 && (pl.tile_pairs - 1) * per < each; ++per) {
+        long long last = std::min(each - (pl.tile_pairs - 1) * per, tiles_kv);
+        const double us_full = per ? full_us * static_cast<double>(up(tiles_kv, per)) : 0.0;
+        const double us = 4.5 + std::max(us_full, last_us * static_cast<double>(up(tiles_kv, last)));
+        if (us < pl.us) {
+            last = up(tiles_kv, up(tiles_kv, last));  // no more CTAs than that time takes
+            pl.us = us;
+            pl.per_list = static_cast<int>(per);
+            pl.per_last = static_cast<int>(last);
+            pl.ctas = static_cast<int>(heads * pl.per_head());
+        }
+        if (pl.tile_pairs == 1 || per >= tiles_kv)
+            break;
+    }
     return pl;
 }
 
@@ -1244,7 +1293,6 @@ SuffixPlan suffix_plan(int B, int Hq, int Hkv, int max_seq_len, int ctas)
     // prefix.
     const long long want = (pl.units + kSuffixMinUnits - 1) / kSuffixMinUnits;
     pl.ctas = static_cast<int>(want < 1 ? 1 : want < ctas ? want : ctas);
-    pl.piece_floats = static_cast<size_t>(2) * pl.ctas * kSuffixWarps * suffix_piece(pl.heads_per_pair);
     return pl;
 }
 
@@ -1312,6 +1360,8 @@ cudaError_t launch_prefix_decode(const PrefixArgs &a, const SuffixArgs *own, cud
     p.part_o = a.part_o;
     p.part_lse = a.part_lse;
     p.ctas = pl.ctas;
+    p.per_list = pl.per_list;
+    p.per_last = pl.per_last;
     constexpr int kSmem = C::kSmem > suffix::kSmem ? C::kSmem : suffix::kSmem;
     static bool set[2][kMaxDevices] = {};
     auto launch = [&](auto kernel, bool (&done)[kMaxDevices]) {

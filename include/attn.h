@@ -501,7 +501,8 @@ int attn_decode_prefix(const void *q, const void *k_pages, const void *v_pages, 
                        float scale, void *stream);
 
 /* attn_decode_prefix_workspace — bytes of workspace that attn_decode_prefix needs for these sizes on the
- * current device (it grows with each of them), or a negative attn_status. */
+ * current device, or a negative attn_status. For given Hq and Hkv it does not shrink as B or a length
+ * grows: a workspace for the largest call serves the smaller ones. */
 long long attn_decode_prefix_workspace(int B, int Hq, int Hkv, int max_prefix_len, int max_seq_len);
 
 #ifdef __cplusplus

@@ -257,6 +257,21 @@ def test_streams_and_graphs():
             assert rep.ok(), (step, b, rep)
 
 
+def test_one_workspace_for_smaller_calls():
+    """A workspace for the largest batch and lengths serves every smaller call, whatever plan that takes."""
+    Hq, Hkv = 8, 2
+    ws = attn.decode_prefix_workspace(40, Hq, Hkv, 5000, 600)
+    for B, plen, longest in ((1, 1, 1), (3, 130, 17), (17, 2000, 600), (40, 5000, 64), (33, 300, 300)):
+        need = attn.decode_prefix_workspace(B, Hq, Hkv, plen, longest).numel()
+        assert need <= ws.numel()
+        lens = [int(x) for x in np.random.RandomState(B).randint(0, longest + 1, size=B)]
+        q, pre, suf, pages, ptab, table = make(B, Hq, Hkv, plen, lens, 64, seed=B)
+        o, lse = call(q, pages, ptab, plen, table, lens, max_prefix_len=plen, max_seq_len=longest, workspace=ws)
+        for b in range(0, B, 5):
+            rep = compare(o[b:b + 1], lse[b:b + 1], *expect(q, pre, suf, lens, b, D ** -0.5))
+            assert rep.ok(), rep
+
+
 def test_refusals():
     B, Hq, Hkv, page, lens = 2, 8, 2, 16, [5, 6]
     q, pre, suf, pages, ptab, table = make(B, Hq, Hkv, 40, lens, page, seed=11)
