@@ -552,22 +552,16 @@ def _rows(name, t, dev, like=None):
     raise ValueError(f"{name} must live on cuda:{dev}, got {t.device}")
 
 
-class _Launch:
-    """The device of a call's tensors made current for the call (when it is not), and the stream."""
-    __slots__ = ("guard", "handle")
-
-    def __init__(self, index, stream):
-        self.handle = _stream_handle(torch.cuda.current_stream(index) if stream is None else stream)
-        self.guard = None if torch.cuda.current_device() == index else torch.cuda.device(index)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self.handle
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _call(fn, dev, stream, *args):
+    """The library call `fn` with device `dev` current and its stream (the current one unless given) last."""
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_handle(stream)
+    if torch.cuda.current_device() == dev:
+        rc = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, handle)
+    if rc != ATTN_OK:
+        raise AttnError(rc, status_string(rc))
 
 
 def _ptr(t):
@@ -640,11 +634,8 @@ def attn_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor | None
     k_out = _new_rows(k) if k_out is None else k_out
     _, qos = _rows("q_out", q_out, dev, qshape)
     _, kos = _rows("k_out", k_out, dev, kshape)
-    with _Launch(dev, stream) as handle:
-        rc = load_library().attn_qk_norm_rope(
-            q.data_ptr(), k.data_ptr(), qw, kw, _ptr(cos), _ptr(sin), pos, q_out.data_ptr(), k_out.data_ptr(), B, Hq, Hkv,
-            S, D, qs, ks, qos, kos, rot_dim, max_pos, 1 if interleaved else 0, eps, handle)
-    _check(rc)
+    _call(load_library().attn_qk_norm_rope, dev, stream, q.data_ptr(), k.data_ptr(), qw, kw, _ptr(cos), _ptr(sin), pos,
+          q_out.data_ptr(), k_out.data_ptr(), B, Hq, Hkv, S, D, qs, ks, qos, kos, rot_dim, max_pos, 1 if interleaved else 0, eps)
     return q_out, k_out
 
 
@@ -673,17 +664,14 @@ def attn_qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor | 
     _, dqs = _rows("dq", dq, dev, qshape)
     _, dks = _rows("dk", dk, dev, kshape)
     dwq = dwk = ws = None
-    with _Launch(dev, stream) as handle:
-        if qw is not None:
-            # One block for the weights' gradients (rows of 16-byte aligned floats), one for the kernels.
-            dwq, dwk = torch.empty((2, D), dtype=torch.float32, device=q.device).unbind(0)
-            ws = torch.empty((_NORM_ROPE_BWD_BLOCKS * 2 * D,), dtype=torch.float32, device=q.device)
-            _used_on(stream, dwq, ws)
-        rc = load_library().attn_qk_norm_rope_bwd(
-            q.data_ptr(), k.data_ptr(), qw, kw, _ptr(cos), _ptr(sin), pos, dq_out.data_ptr(), dk_out.data_ptr(),
-            dq.data_ptr(), dk.data_ptr(), _ptr(dwq), _ptr(dwk), _ptr(ws), B, Hq, Hkv, S, D, qs, ks, dqos, dkos, dqs, dks,
-            rot_dim, max_pos, 1 if interleaved else 0, eps, handle)
-    _check(rc)
+    if qw is not None:
+        # One block for the weights' gradients (rows of 16-byte aligned floats), one for the kernels.
+        dwq, dwk = torch.empty((2, D), dtype=torch.float32, device=q.device).unbind(0)
+        ws = torch.empty((_NORM_ROPE_BWD_BLOCKS * 2 * D,), dtype=torch.float32, device=q.device)
+        _used_on(stream, dwq, ws)
+    _call(load_library().attn_qk_norm_rope_bwd, dev, stream, q.data_ptr(), k.data_ptr(), qw, kw, _ptr(cos), _ptr(sin), pos,
+          dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), _ptr(dwq), _ptr(dwk), _ptr(ws), B, Hq, Hkv, S,
+          D, qs, ks, dqos, dkos, dqs, dks, rot_dim, max_pos, 1 if interleaved else 0, eps)
     return dq, dk, dwq, dwk
 
 
@@ -723,16 +711,11 @@ def _append(k, v, cos, sin, k_pages, v_pages, k_scale, v_scale, block_table, seq
     elif q_out is not None:
         raise ValueError("q_out without q")
     lib = load_library()
-    head = (_ptr(q), k.data_ptr(), v.data_ptr(), qw, kw, _ptr(cos), _ptr(sin), pos, seq_lens.data_ptr(),
-            _ptr(new_lens), block_table.data_ptr(), _ptr(q_out), k_pages.data_ptr(), v_pages.data_ptr())
-    with _Launch(dev, stream) as handle:
-        tail = (B, Hq, Hkv, Sq, qs, ks, vs, qos, num_pages, page_size, per_seq, rot_dim, max_pos,
-                1 if interleaved else 0, eps, handle)
-        if fp8:
-            rc = lib.attn_append_paged_fp8(*head, k_scale.data_ptr(), v_scale.data_ptr(), *tail)
-        else:
-            rc = lib.attn_append_paged(*head, *tail)
-    _check(rc)
+    scales = (k_scale.data_ptr(), v_scale.data_ptr()) if fp8 else ()
+    _call(lib.attn_append_paged_fp8 if fp8 else lib.attn_append_paged, dev, stream, _ptr(q), k.data_ptr(), v.data_ptr(), qw,
+          kw, _ptr(cos), _ptr(sin), pos, seq_lens.data_ptr(), _ptr(new_lens), block_table.data_ptr(), _ptr(q_out),
+          k_pages.data_ptr(), v_pages.data_ptr(), *scales, B, Hq, Hkv, Sq, qs, ks, vs, qos, num_pages, page_size, per_seq,
+          rot_dim, max_pos, 1 if interleaved else 0, eps)
     return q_out
 
 
@@ -816,12 +799,10 @@ def attn_decode_prefix(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Te
         workspace = decode_prefix_workspace(B, Hq, Hkv, max_prefix_len, max_seq_len, q.device)
         _used_on(stream, workspace)
     ws_bytes, = _flat("workspace", workspace, torch.uint8, 1, dev)
-    with _Launch(dev, stream) as handle:
-        rc = load_library().attn_decode_prefix(
-            q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), prefix_table.data_ptr(), prefix_len.data_ptr(),
-            block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), ws_bytes,
-            B, Hq, Hkv, num_pages, page_size, prefix_pages, max_prefix_len, per_seq, max_seq_len, scale, handle)
-    _check(rc)
+    _call(load_library().attn_decode_prefix, dev, stream, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+          prefix_table.data_ptr(), prefix_len.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
+          lse.data_ptr(), workspace.data_ptr(), ws_bytes, B, Hq, Hkv, num_pages, page_size, prefix_pages, max_prefix_len,
+          per_seq, max_seq_len, scale)
     return out, lse
 
 

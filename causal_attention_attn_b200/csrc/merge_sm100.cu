@@ -196,11 +196,13 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const Pr
             find_part(k + lane * kSplit + warp, &o, &lse);
         const float l = lse ? __ldcg(lse) : -INFINITY;
         const int parts = min(32, (n - k - warp + kSplit - 1) / kSplit);
-        // Eight parts' rows at a time, the first eight sent for before their weights are known.
-        float4 v[8];
+        // Eight parts' rows at a time, the first eight sent for before their weights are known (16 at a time
+        // took longer: fewer blocks fit an SM).
+        constexpr int kFlight = 8;
+        float4 v[kFlight];
         auto fetch = [&](int t) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < kFlight; ++j) {
                 const float *po = reinterpret_cast<const float *>(
                     __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), min(t + j, 31)));
                 v[j] = t + j < parts ? __ldcg(reinterpret_cast<const float4 *>(po) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -218,11 +220,11 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const Pr
         M = new_m;
         // fmaxf drops NaN: a part with a NaN LSE (from NaN scores) keeps a NaN weight.
         const float w = l == -INFINITY ? 0.f : exp2f(l - M);
-        for (int t = 0; t < parts; t += 8) {
+        for (int t = 0; t < parts; t += kFlight) {
             if (t > 0)
                 fetch(t);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < kFlight; ++j) {
                 const float wt = __shfl_sync(0xffffffffu, w, min(t + j, 31)), u = t + j < parts ? wt : 0.f;
                 if (u != 0.f) {  // a part of weight 0 may hold anything (all its scores -inf)
                     acc.x = fmaf(u, v[j].x, acc.x);

@@ -43,7 +43,7 @@ namespace suffix {
 constexpr int kD = 128;
 constexpr int kKeys = kSuffixUnitKeys;  // keys of a unit
 constexpr int kWarps = kSuffixWarps;
-constexpr int kStages = 2;
+constexpr int kStages = 2;  // (8 workers x 3, 6 x 4 and 4 x 6 were 2 to 18% slower over the longer suffixes)
 constexpr int kBoxBytes = kKeys * 128;        // 16 keys x 64 dims
 constexpr int kStageBytes = 4 * kBoxBytes;    // K dims 0-63, 64-127, then V
 constexpr int kOffBar = kWarps * kStages * kStageBytes;
@@ -188,6 +188,7 @@ __device__ __forceinline__ void run(const CUtensorMap &tm_k, const CUtensorMap &
     };
 
     // Copies: lane 0 keeps a cursor ahead of the one that computes, and the next unit's page with it.
+    const uint64_t pol = l2_policy_evict_first();  // read once: the prefix's partials stay in L2 instead
     Cursor ahead = first;
     int issued = 0, page = 0, in_page = 0;
     auto look_up = [&]() {
@@ -202,10 +203,10 @@ __device__ __forceinline__ void run(const CUtensorMap &tm_k, const CUtensorMap &
         if (page < 0 || page >= p.num_pages)
             page = p.num_pages;  // behind the last page: zeros
         mbar_arrive_expect_tx(bar, kStageBytes);
-        tma_load_4d(dst, &tm_k, bar, 0, in_page, kvh, page);
-        tma_load_4d(dst + kBoxBytes, &tm_k, bar, 64, in_page, kvh, page);
-        tma_load_4d(dst + 2 * kBoxBytes, &tm_v, bar, 0, in_page, kvh, page);
-        tma_load_4d(dst + 3 * kBoxBytes, &tm_v, bar, 64, in_page, kvh, page);
+        tma_load_4d_hint(dst, &tm_k, bar, 0, in_page, kvh, page, pol);
+        tma_load_4d_hint(dst + kBoxBytes, &tm_k, bar, 64, in_page, kvh, page, pol);
+        tma_load_4d_hint(dst + 2 * kBoxBytes, &tm_v, bar, 0, in_page, kvh, page, pol);
+        tma_load_4d_hint(dst + 3 * kBoxBytes, &tm_v, bar, 64, in_page, kvh, page, pol);
         if (++issued < n_units) {
             if (++ahead.unit == ahead.units)
                 next_pair(ahead);
