@@ -137,31 +137,44 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendParams 
             w = unpack_pairs<kInterleaved>(load_row(sc.w, le));
             have_w = kind;
         }
-        Angles ang;
-        if (turn)
-            ang = read_angles(base + kAngles * kSlotBytes);
+        // Everything of the stage is read, and the row sums of both rows are taken, before anything is
+        // stored: the two rows' chains then overlap.
+        Pairs x[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            x[k] = unpack_pairs<kInterleaved>(read_row(base + k * kRowSlots * kSlotBytes));
+        if (norm) {
+            float r[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                r[k] = row_sum<kD>(pairs_dot(x[k], x[k]));
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                scale_pairs(x[k], rsqrtf(r[k] * (1.f / kD) + p.eps), w);
+        }
+        if (turn) {
+            const Angles ang = read_angles(base + kAngles * kSlotBytes);
+            rotate_pairs<false>(x[0], ang);
+            rotate_pairs<false>(x[1], ang);
+        }
+        if (kind == kQ) {
+            __nv_bfloat16 *out = p.q_out + (a.b * p.qos.b + a.h * p.qos.h + a.i * p.qos.s);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                if (k ? a.live1 : a.live0)
+                    store_row(out + (k ? p.qos.h : 0), le, write ? pack_pairs<kInterleaved>(x[k]) : zero_row());
+            return;
+        }
+        if (!write)
+            return;
+        const size_t dst = ((static_cast<size_t>(a.page) * p.Hkv + a.h) * p.page_size.d + a.slot) * kD;
+        const size_t next_head = static_cast<size_t>(p.page_size.d) * kD;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const bool live = k ? a.live1 : a.live0;
-            const uint32_t h = a.h + k;
-            Pairs x = unpack_pairs<kInterleaved>(read_row(base + k * kRowSlots * kSlotBytes));
-            if (norm) {
-                const float r = rsqrtf(row_sum<kD>(pairs_dot(x, x)) * (1.f / kD) + p.eps);
-                scale_pairs(x, r, w);
-            }
-            if (turn)
-                rotate_pairs<false>(x, ang);
-            if (kind == kQ) {
-                if (live)
-                    store_row(p.q_out + (a.b * p.qos.b + h * p.qos.h + a.i * p.qos.s), le,
-                              write ? pack_pairs<kInterleaved>(x) : zero_row());
+            if (!(k ? a.live1 : a.live0))
                 continue;
-            }
-            if (!write || !live)
-                continue;
-            const size_t dst = ((static_cast<size_t>(a.page) * p.Hkv + h) * p.page_size.d + a.slot) * kD;
             if constexpr (kFp8) {
-                const float *cf = p.coef[kind - kK] + h * kD;
+                const float *cf = p.coef[kind - kK] + (a.h + k) * kD;
                 uint32_t codes[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {  // four elements at a time, in element order
@@ -170,15 +183,16 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendParams 
 #pragma unroll
                     for (int t = 0; t < 4; ++t) {
                         const int e = 4 * j + t;  // of the lane's sixteen
-                        v[t] = kInterleaved ? ((e & 1) ? x.B[e >> 1] : x.A[e >> 1]) : (e < 8 ? x.A[e & 7] : x.B[e & 7]);
+                        v[t] = kInterleaved ? ((e & 1) ? x[k].B[e >> 1] : x[k].A[e >> 1]) : (e < 8 ? x[k].A[e & 7] : x[k].B[e & 7]);
                     }
                     codes[j] = e4m3x4(__fdividef(v[0], f.x), __fdividef(v[1], f.y), __fdividef(v[2], f.z), __fdividef(v[3], f.w));
                 }
-                uint8_t *out = static_cast<uint8_t *>(p.pages[kind - kK]) + dst;
+                uint8_t *out = static_cast<uint8_t *>(p.pages[kind - kK]) + dst + (k ? next_head : 0);
                 *reinterpret_cast<uint2 *>(out + le.e0) = make_uint2(codes[0], codes[1]);
                 *reinterpret_cast<uint2 *>(out + le.e1) = make_uint2(codes[2], codes[3]);
             } else {
-                store_row(static_cast<__nv_bfloat16 *>(p.pages[kind - kK]) + dst, le, pack_pairs<kInterleaved>(x));
+                store_row(static_cast<__nv_bfloat16 *>(p.pages[kind - kK]) + dst + (k ? next_head : 0), le,
+                          pack_pairs<kInterleaved>(x[k]));
             }
         }
     };

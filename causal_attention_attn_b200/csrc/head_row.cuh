@@ -234,6 +234,16 @@ __device__ __forceinline__ Angles read_angles(uint32_t src)
 __device__ __forceinline__ float2 two(const float *x) { return make_float2(x[0], x[1]); }
 __device__ __forceinline__ void put_two(float *x, float2 v) { x[0] = v.x, x[1] = v.y; }
 
+// x <- x w.
+__device__ __forceinline__ void mul_pairs(Pairs &x, const Pairs &w)
+{
+#pragma unroll
+    for (int u = 0; u < 8; u += 2) {
+        put_two(x.A + u, __fmul2_rn(two(x.A + u), two(w.A + u)));
+        put_two(x.B + u, __fmul2_rn(two(x.B + u), two(w.B + u)));
+    }
+}
+
 // x <- x r w.
 __device__ __forceinline__ void scale_pairs(Pairs &x, float r, const Pairs &w)
 {

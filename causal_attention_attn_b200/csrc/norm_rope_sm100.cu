@@ -97,8 +97,12 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_kernel(const NormRopePa
     const int step = gridDim.x * kWarps;
     const int first = blockIdx.x * kWarps + warp;
 
-    // Starts the copies of one unit into stage s; an empty group behind the last unit.
-    PairAt at[G::kStages];
+    // Starts the copies of one unit into stage s; an empty group behind the last unit. What is left for
+    // consume: where the pair's output goes, and whether its rows exist and their position has angles.
+    struct Sent {
+        long long out;
+        bool live0, live1, has;
+    } sent[G::kStages];
     auto issue = [&](int unit, int s) {
         if (unit < n_units) {
             const bool is_k = unit >= n_q;
@@ -106,21 +110,24 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_kernel(const NormRopePa
             uint32_t tok;
             PairAt a = locate_pair(sd, p.seq, (unit - (is_k ? n_q : 0)) * R::kRows + group, &tok);
             const uint32_t base = ring + static_cast<uint32_t>(s * G::kStageBytes);
+            const int pos = p.positions ? __ldg(p.positions + tok) : static_cast<int>(a.i);
+            a.has = p.table.has(pos);
+            // A row that does not exist, or whose position has no row of the tables, arrives as zeros (and
+            // gives zeros: consume takes r as 0 there).
+            const bool on0 = a.live0 && a.has, on1 = a.live1 && a.has;
             if (kBackward) {
                 const __nv_bfloat16 *dz = sd.dz + a.offset(sd.zs);
-                copy_row(base + G::kDz * kSlotBytes, dz, le, a.live0);
-                copy_row(base + (G::kDz + kRowSlots) * kSlotBytes, a.live1 ? dz + sd.zs.h : dz, le, a.live1);
+                copy_row(base + G::kDz * kSlotBytes, dz, le, on0);
+                copy_row(base + (G::kDz + kRowSlots) * kSlotBytes, on1 ? dz + sd.zs.h : dz, le, on1);
             }
             if (!kBackward || sd.w) {
                 const __nv_bfloat16 *x = sd.x + a.offset(sd.xs);
-                copy_row(base + G::kX * kSlotBytes, x, le, a.live0);
-                copy_row(base + (G::kX + kRowSlots) * kSlotBytes, a.live1 ? x + sd.xs.h : x, le, a.live1);
+                copy_row(base + G::kX * kSlotBytes, x, le, on0);
+                copy_row(base + (G::kX + kRowSlots) * kSlotBytes, on1 ? x + sd.xs.h : x, le, on1);
             }
-            const int pos = p.positions ? __ldg(p.positions + tok) : static_cast<int>(a.i);
-            a.has = p.table.has(pos);
             if (le.rotated && a.has)
                 copy_angles(base + G::kAngles * kSlotBytes, p.table, pos, l);
-            at[s] = a;
+            sent[s] = Sent{a.offset(sd.os), a.live0, a.live1, a.has};
         }
         copy_commit();
     };
@@ -169,46 +176,61 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_kernel(const NormRopePa
         const Side &sd = p.side[is_k ? 1 : 0];
         const bool norm = sd.w != nullptr;
         const uint32_t base = ring + static_cast<uint32_t>(s * G::kStageBytes);
-        const PairAt a = at[s];
+        const Sent a = sent[s];
         const bool turn = le.rotated && a.has;
-        __nv_bfloat16 *out = sd.out + a.offset(sd.os);
-        Angles ang;
-        if (turn)
-            ang = read_angles(base + G::kAngles * kSlotBytes);
+        __nv_bfloat16 *out = sd.out + a.out;
+        // Everything of the stage is read, and the row sums of both rows are taken, before anything is
+        // stored: the two rows' chains then overlap.
+        if constexpr (!kBackward) {
+            Pairs x[2];
+            float r[2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const bool live = k ? a.live1 : a.live0;
-            // A position without a row of the tables: zeros out, and no gradient.
-            const bool in = live && a.has;
-            if constexpr (!kBackward) {
-                Pairs x = unpack_pairs<kInterleaved>(read_row(base + (G::kX + k * kRowSlots) * kSlotBytes));
-                if (norm) {
-                    const float r = rsqrtf(row_sum<D>(pairs_dot(x, x)) * (1.f / D) + p.eps);
-                    scale_pairs(x, r, w);
-                }
+            for (int k = 0; k < 2; ++k)
+                x[k] = unpack_pairs<kInterleaved>(read_row(base + (G::kX + k * kRowSlots) * kSlotBytes));
+            Angles ang;
+            if (turn)
+                ang = read_angles(base + G::kAngles * kSlotBytes);
+            if (norm) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    r[k] = row_sum<D>(pairs_dot(x[k], x[k]));
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    scale_pairs(x[k], a.has ? rsqrtf(r[k] * (1.f / D) + p.eps) : 0.f, w);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
                 if (turn)
-                    rotate_pairs<false>(x, ang);
-                if (live)
-                    store_row(out + (k ? sd.os.h : 0), le, in ? pack_pairs<kInterleaved>(x) : zero_row());
-            } else {
-                const RawRow dr = read_row(base + (G::kDz + k * kRowSlots) * kSlotBytes);
-                Pairs dy = unpack_pairs<kInterleaved>(in ? dr : zero_row());
+                    rotate_pairs<false>(x[k], ang);
+                if (k ? a.live1 : a.live0)
+                    store_row(out + (k ? sd.os.h : 0), le, pack_pairs<kInterleaved>(x[k]));
+            }
+        } else {
+            // (One row after the other: both at once need more than 128 registers, and spilling took 1.7
+            // times as long.)
+            Angles ang;
+            if (turn)
+                ang = read_angles(base + G::kAngles * kSlotBytes);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const bool live = k ? a.live1 : a.live0;
+                Pairs dy = unpack_pairs<kInterleaved>(read_row(base + (G::kDz + k * kRowSlots) * kSlotBytes));
                 if (turn)
                     rotate_pairs<true>(dy, ang);
                 if (norm) {
-                    const RawRow xr = read_row(base + (G::kX + k * kRowSlots) * kSlotBytes);
-                    const Pairs x = unpack_pairs<kInterleaved>(in ? xr : zero_row());
+                    const Pairs x = unpack_pairs<kInterleaved>(read_row(base + (G::kX + k * kRowSlots) * kSlotBytes));
                     Pairs g = dy;
-                    scale_pairs(g, 1.f, unpack_pairs<kInterleaved>(wraw));
+                    mul_pairs(g, unpack_pairs<kInterleaved>(wraw));
                     const float xx = row_sum<D>(pairs_dot(x, x)), gx = row_sum<D>(pairs_dot(g, x));
-                    const float r = in ? rsqrtf(xx * (1.f / D) + p.eps) : 0.f;
-                    const float f = r * r * (gx * (1.f / D));
+                    const float r = live && a.has ? rsqrtf(xx * (1.f / D) + p.eps) : 0.f;
+                    const float f = -r * r * (gx * (1.f / D));
+                    const float2 rr = make_float2(r, r), ff = make_float2(f, f);
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        dw.A[u] = fmaf(dy.A[u], x.A[u] * r, dw.A[u]);
-                        dw.B[u] = fmaf(dy.B[u], x.B[u] * r, dw.B[u]);
-                        dy.A[u] = r * fmaf(-f, x.A[u], g.A[u]);
-                        dy.B[u] = r * fmaf(-f, x.B[u], g.B[u]);
+                    for (int u = 0; u < 8; u += 2) {
+                        put_two(dw.A + u, __ffma2_rn(two(dy.A + u), __fmul2_rn(two(x.A + u), rr), two(dw.A + u)));
+                        put_two(dw.B + u, __ffma2_rn(two(dy.B + u), __fmul2_rn(two(x.B + u), rr), two(dw.B + u)));
+                        put_two(dy.A + u, __fmul2_rn(rr, __ffma2_rn(ff, two(x.A + u), two(g.A + u))));
+                        put_two(dy.B + u, __fmul2_rn(rr, __ffma2_rn(ff, two(x.B + u), two(g.B + u))));
                     }
                 }
                 if (live)
