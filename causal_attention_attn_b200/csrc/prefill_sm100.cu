@@ -908,8 +908,9 @@ __device__ __forceinline__ void run_tiles(const CUtensorMap &tm_q, const CUtenso
                 bool rescale = false;
                 if (j == 0) {
                     // Key 0 is visible to every row, so this is finite; with a paged cache a row may
-                    // see no key yet, and the floor keeps its weights 2^(-inf) = 0.
-                    m = kPaged ? fmaxf(mx2, kNoKeyMax) : mx2;
+                    // see no key yet (and a segment of a prefix only keys of score -inf), and the floor
+                    // keeps its weights 2^(-inf) = 0.
+                    m = kPages ? fmaxf(mx2, kNoKeyMax) : mx2;
                 } else {
                     const float m_new = fmaxf(m, mx2);
                     rescale = __any_sync(0xffffffffu, m_new > m + kRescaleThreshold);
@@ -978,7 +979,7 @@ __device__ __forceinline__ void run_tiles(const CUtensorMap &tm_q, const CUtenso
                 break;
             tc_fence_after_sync();
             // Paged: a row that saw no key has l = 0: O = 0 and LSE = m + log2(0) = -inf.
-            const float inv_l = (kPaged && !(l_pv > 0.f)) ? 0.f : 1.f / l_pv;
+            const float inv_l = (kPages && !(l_pv > 0.f)) ? 0.f : 1.f / l_pv;
             if constexpr (kMode == kPrefix) {
                 // Partials: normalised O in fp32, 32 dims at a time turned in the warp's staging box (16-byte
                 // units XOR row % 8) so that eight lanes store one row's 128 bytes, and the LSE in log2

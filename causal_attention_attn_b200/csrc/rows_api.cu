@@ -59,8 +59,9 @@ int norm_rope(const void *q, const void *k, const void *q_weight, const void *k_
     const bool want_dw = dq_weight || dk_weight;
     if (want_dw && !workspace)
         return ATTN_ERR_NULL;
+    const bool uses[6] = {q != nullptr, k != nullptr, backward, backward, true, true};
     for (int i = 0; i < 6; ++i)
-        if (!strides[i] && (backward || (i != 2 && i != 3)))
+        if (!strides[i] && uses[i])
             return ATTN_ERR_NULL;
     if (B < 1 || Hq < 1 || Hkv < 1 || S < 1 || D < 1)
         return ATTN_ERR_SHAPE;

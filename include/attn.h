@@ -380,7 +380,8 @@ int attn_lse_merge(float *o_acc, float *lse_acc, const void *o_part, const float
  *   D                32, 64 or 128. rot_dim: a multiple of 16 in [0, D].
  *   eps              finite and >= 0.
  * Hq and Hkv need not divide one another here. Pointers 16-byte aligned (positions: 4). Never
- * allocates or synchronises; returns ATTN_OK or a negative attn_status (before any launch).
+ * allocates or synchronises; the first call on a device comes before any stream capture. Returns
+ * ATTN_OK or a negative attn_status (before any launch).
  */
 int attn_qk_norm_rope(const void *q, const void *k, const void *q_weight, const void *k_weight, const float *cos,
                       const float *sin, const int *positions, void *q_out, void *k_out, int B, int Hq, int Hkv, int S,
@@ -401,8 +402,8 @@ int attn_qk_norm_rope(const void *q, const void *k, const void *q_weight, const 
  *   workspace             ATTN_QK_NORM_ROPE_BWD_WORKSPACE(D) bytes on the device, 16-byte aligned,
  *                         owned by the caller and used only until the call's work is done; may be NULL
  *                         when neither weight gradient is wanted. Calls that overlap need one each.
- * A token whose position has no row of the tables has zero gradients. Without weights q and k may
- * be NULL. Other arguments, rules and errors as attn_qk_norm_rope.
+ * A token whose position has no row of the tables has zero gradients. Without weights q and k (and
+ * their strides) may be NULL. Other arguments, rules and errors as attn_qk_norm_rope.
  */
 #define ATTN_QK_NORM_ROPE_BWD_WORKSPACE(D) (592u * 2u * 4u * (unsigned)(D))
 int attn_qk_norm_rope_bwd(const void *q, const void *k, const void *q_weight, const void *k_weight, const float *cos,

@@ -176,6 +176,28 @@ def test_one_sequences_nan_stays_its_own():
     assert torch.isnan(o[2, 1]).all() and torch.isnan(o[5, :4]).all() and not torch.isfinite(o[4, 4:]).any()
 
 
+def test_keys_of_score_minus_infinity():
+    """Keys with -inf where every query is positive have scores of -inf: weight 0. A whole KV tile of the
+    prefix, a whole unit of a suffix, and in one sequence every key there is but the prefix's."""
+    B, Hq, Hkv, page, lens = 3, 8, 2, 64, [40, 16, 33]
+    q, pre, suf, pages, ptab, table = make(B, Hq, Hkv, 300, lens, page, seed=12)
+    q[..., 0] = 1.0
+    inf = float("-inf")
+    drop_pre = range(0, 128)
+    drop_suf = {0: range(16, 32), 1: range(0, 16)}
+    for j in drop_pre:
+        pages[0][ptab[j // page], :, j % page, 0] = inf
+    for b, keys in drop_suf.items():
+        for j in keys:
+            pages[0][table[b, j // page], :, j % page, 0] = inf
+    o, lse = call(q, pages, ptab, 300, table, lens, max_prefix_len=300, max_seq_len=40)
+    for b in range(B):
+        keep = [j for j in range(lens[b]) if j not in drop_suf.get(b, ())]
+        k, v = (torch.cat((p[:, 128:], s[b, :, keep]), dim=1)[None] for p, s in zip(pre, suf))
+        rep = compare(o[b:b + 1], lse[b:b + 1], *oracle.attention(q[b:b + 1], k, v, D ** -0.5, True))
+        assert rep.ok(), (b, rep)
+
+
 def test_agrees_with_the_paged_decode_and_repeats():
     """The same keys through attn_decode_paged, with the prefix's pages in every sequence's table."""
     B, Hq, Hkv, page, plen = 12, 32, 8, 64, 640

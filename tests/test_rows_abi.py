@@ -96,6 +96,15 @@ def append(lib, fp8=False, **kw):
     return fn(*p.values(), *a.values(), *st, *b.values(), None)
 
 
+def test_backward_without_a_norm_takes_no_inputs(lib):
+    """No q, k or strides of theirs: the arguments pass, and the call fails only where there is no GPU."""
+    if torch.cuda.is_available():
+        pytest.skip("would reach the device with fake pointers")
+    none = dict(q=None, k=None, qw=None, kw=None, dqw=None, dkw=None, ws=None)
+    assert backward(lib, qs=None, ks=None, **none) in (-12, -7)
+    assert backward(lib, qs=None, ks=None, dqs=None, **none) == -1
+
+
 @pytest.mark.parametrize("name,over,expected", [
     ("null v", dict(v=None), -1),
     ("null lengths", dict(lens=None), -1),
