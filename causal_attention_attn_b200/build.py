@@ -23,7 +23,7 @@ LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ["attn_api.cu", "prefill_sm100.cu", "prefill_fp8_sm100.cu", "decode_sm100.cu", "decode_tc_sm100.cu", "bwd_sm100.cu",
            "merge_sm100.cu", "attn_noalloc.cu", "rows_api.cu", "norm_rope_sm100.cu", "append_sm100.cu"]
 HEADERS = ["kernels.h", "sm100_ptx.cuh", "tma_host.h", "head_row.cuh", "fast_div.h",
-           "suffix_sm100.cuh"]
+           "suffix_sm100.cuh", "prefix_split.cuh"]
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
 

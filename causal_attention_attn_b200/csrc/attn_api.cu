@@ -739,14 +739,13 @@ namespace {
 
 // attn_decode_prefix's workspace, cut up.
 struct PrefixSpace {
-    size_t pieces, o_suffix, lse_suffix, part_o, part_lse, bytes;  // byte offsets
+    size_t split, pieces, o_suffix, lse_suffix, part_o, part_lse, bytes;  // byte offsets
 };
 
-// Sized for as many CTAs as the device has SMs, whatever the plan takes of them, so that a workspace for
-// larger batches and lengths serves smaller ones.
-PrefixSpace prefix_space(int B, int Hq, const PrefixPlan &pl, const SuffixPlan &suffix, int sm_count)
+// Sized for the whole grid on either part: the lengths, which divide it, are known on the device only.
+PrefixSpace prefix_space(int B, int Hq, const PrefixPlan &pl, const SuffixPlan &suffix)
 {
-    const size_t slots = static_cast<size_t>(pl.lists) + sm_count;
+    const size_t slots = static_cast<size_t>(pl.lists) + pl.grid;
     size_t at = 0;
     auto take = [&](size_t n) {
         const size_t here = at;
@@ -755,7 +754,8 @@ PrefixSpace prefix_space(int B, int Hq, const PrefixPlan &pl, const SuffixPlan &
     };
     PrefixSpace sp;
     const size_t rows = static_cast<size_t>(B) * Hq;
-    sp.pieces = take(sizeof(float) * 2 * sm_count * kSuffixWarps * suffix_piece(suffix.heads_per_pair));
+    sp.split = take(sizeof(PrefixSplit));
+    sp.pieces = take(sizeof(float) * 2 * pl.grid * kSuffixWarps * suffix_piece(suffix.heads_per_pair));
     sp.o_suffix = take(rows * 128 * sizeof(float));
     sp.lse_suffix = take(rows * sizeof(float));
     sp.part_o = take(slots * 256 * 128 * sizeof(float));
@@ -776,38 +776,6 @@ int check_prefix_sizes(int B, int Hq, int Hkv, int max_prefix_len, int max_seq_l
     return ATTN_OK;
 }
 
-// Both plans and the workspace's parts on the current device (g_mutex held).
-int plan_prefix(const DeviceState &s, int B, int Hq, int Hkv, int max_prefix_len, int max_seq_len, PrefixPlan *pl,
-                SuffixPlan *suffix, PrefixSpace *sp)
-{
-    *pl = prefix_plan(B, Hq, Hkv, max_prefix_len, s.sm_count);
-    *suffix = suffix_plan(B, Hq, Hkv, max_seq_len, s.sm_count);
-    if (max_seq_len > 0 && max_prefix_len > 0) {
-        // Side by side where that costs the prefix little: the fewer CTAs it takes, the more SMs are left
-        // for the suffixes, if they are done there before it is. Measured: the suffixes take 3.4 us and
-        // 0.112 us for each unit of an SM (8 KB at 73 GB/s); in turn they cost 4 us at the least, so the
-        // prefix may lose that much. Both lengths are bounds here: a shorter suffix leaves SMs idle that the
-        // prefix did without.
-        const double least = pl->us;
-        auto suffix_us = [&](int sms) { return 3.4 + 0.112 * static_cast<double>(suffix->units) / sms; };
-        for (const double loss : {0.0, 2.0, 4.0}) {
-            const double need = std::ceil(0.112 * static_cast<double>(suffix->units) / (least + loss - 3.4));
-            if (need >= s.sm_count)
-                continue;
-            const PrefixPlan fewer =
-                prefix_plan(B, Hq, Hkv, max_prefix_len, s.sm_count - std::max(1, static_cast<int>(need)));
-            const int rest = s.sm_count - fewer.ctas;
-            if (fewer.us > least + 4.0 || suffix_us(rest) > fewer.us)
-                continue;
-            *pl = fewer;
-            *suffix = suffix_plan(B, Hq, Hkv, max_seq_len, rest);
-            break;
-        }
-    }
-    *sp = prefix_space(B, Hq, *pl, *suffix, s.sm_count);
-    return ATTN_OK;
-}
-
 }  // namespace
 
 extern "C" long long attn_decode_prefix_workspace(int B, int Hq, int Hkv, int max_prefix_len, int max_seq_len)
@@ -820,11 +788,7 @@ extern "C" long long attn_decode_prefix_workspace(int B, int Hq, int Hkv, int ma
     DeviceState *s = device_state(&err);
     if (!s)
         return err;
-    PrefixPlan pl;
-    SuffixPlan suffix;
-    PrefixSpace sp;
-    rc = plan_prefix(*s, B, Hq, Hkv, max_prefix_len, max_seq_len, &pl, &suffix, &sp);
-    return rc != ATTN_OK ? rc : static_cast<long long>(sp.bytes);
+    return static_cast<long long>(prefix_space(B, Hq, prefix_plan(B, Hq, Hkv, s->sm_count), suffix_plan(Hq, Hkv)).bytes);
 }
 
 extern "C" int attn_decode_prefix(const void *q, const void *k_pages, const void *v_pages, const int *prefix_table,
@@ -859,12 +823,9 @@ extern "C" int attn_decode_prefix(const void *q, const void *k_pages, const void
     DeviceState *s = device_state(&err);
     if (!s)
         return err;
-    PrefixPlan pl;
-    SuffixPlan suffix;
-    PrefixSpace sp;
-    rc = plan_prefix(*s, B, Hq, Hkv, max_prefix_len, max_seq_len, &pl, &suffix, &sp);
-    if (rc != ATTN_OK)
-        return rc;
+    const PrefixPlan pl = prefix_plan(B, Hq, Hkv, s->sm_count);
+    const SuffixPlan suffix = suffix_plan(Hq, Hkv);
+    const PrefixSpace sp = prefix_space(B, Hq, pl, suffix);
     if (workspace_bytes < static_cast<long long>(sp.bytes))
         return ATTN_ERR_WORKSPACE;
     // The prefix's units (KV tiles of all lists) and the suffixes' are numbered in 31 bits.
@@ -872,7 +833,7 @@ extern "C" int attn_decode_prefix(const void *q, const void *k_pages, const void
                                           static_cast<long long>(max_prefix_len));
     const long long own_cap = std::min(static_cast<long long>(pages_per_seq) * page_size, static_cast<long long>(max_seq_len));
     const long long own_pairs = static_cast<long long>(B) * Hkv * suffix.head_groups;
-    if (pl.lists > INT_MAX / ((prefix_cap + 127) / 128 + 1) || own_pairs > INT_MAX / (own_cap / kSuffixUnitKeys + 2))
+    if (pl.lists > INT_MAX / ((prefix_cap + 127) / 128 + 1) || own_pairs > INT_MAX / (own_cap / kSuffixUnitKeys + 1 + kSuffixPairUnits))
         return ATTN_ERR_SHAPE;
     if (!s->prefix_status) {
         void *word = nullptr;
@@ -895,9 +856,12 @@ extern "C" int attn_decode_prefix(const void *q, const void *k_pages, const void
     pa.num_pages = num_pages;
     pa.page_size = page_size;
     pa.prefix_pages = prefix_pages;
-    pa.max_prefix_len = max_prefix_len;
+    pa.cap = static_cast<int>(prefix_cap);
     pa.scale = scale;
     pa.plan = pl;
+    const long long own_work = own_cap > 0 ? own_pairs * ((own_cap + kSuffixUnitKeys - 1) / kSuffixUnitKeys + kSuffixPairUnits) : 0;
+    const double us = prefix_split(pl, (prefix_cap + 127) / 128, own_work, &pa.fixed);
+    pa.split = us > kFixedSplitUs ? reinterpret_cast<PrefixSplit *>(at(sp.split)) : nullptr;
     pa.part_o = reinterpret_cast<float *>(at(sp.part_o));
     pa.part_lse = reinterpret_cast<float *>(at(sp.part_lse));
     pa.status = s->prefix_status;
@@ -930,6 +894,8 @@ extern "C" int attn_decode_prefix(const void *q, const void *k_pages, const void
     }
     PrefixMergeArgs m;
     m.plan = pl;
+    m.fixed = pa.fixed;
+    m.split = pa.split;
     m.B = B;
     m.Hq = Hq;
     m.Hkv = Hkv;

@@ -38,10 +38,6 @@ cudaError_t launch_behind(void (*kernel)(Params...), int grid, int threads, size
 struct EvenRange {
     unsigned base, rem;
     __host__ __device__ EvenRange(unsigned total, unsigned parts) : base(total / parts), rem(total - base * parts) {}
-    __host__ __device__ EvenRange(unsigned total, const FastDiv &parts)  // total < 2^31
-        : base(parts.quot(total)), rem(total - base * parts.d)
-    {
-    }
     __host__ __device__ unsigned begin(unsigned c) const { return c * base + (c < rem ? c : rem); }
     // The range that holds unit g < total.
     __host__ __device__ unsigned part_of(unsigned g) const
@@ -169,30 +165,40 @@ cudaError_t launch_prefill_fp8(const PrefillFp8Args &a, cudaStream_t stream, int
 
 // The shared-prefix part of a decode over paged caches (head dim 128): B sequences, one new token each,
 // over the prefix's keys. The packed rows of one kv head make tiles of 128, two tiles share a list of KV
-// tiles, and the lists are cut over `ctas` CTAs; every (list, CTA) segment leaves fp32 partials
-// in slot list + CTA: part_o [slots][2][128][128] normalised, part_lse [slots][2][128] in log2 units.
+// tiles, and the lists are cut over blocks of the grid (prefix_split.cuh); every (list, block) segment
+// leaves fp32 partials in slot list + block: part_o [slots][2][128][128] normalised, part_lse
+// [slots][2][128] in log2 units.
 struct PrefixPlan {
     int group, sub_groups;  // query heads of a row tile's group; parts of a group above 128 heads
+    int heads;              // kv heads times sub_groups
     int tile_seqs;          // sequences in a tile
     int tile_pairs;         // per head
+    int odd;                // a head's last pair has one tile only
     long long lists;
-    long long units;        // KV tiles of all lists, at most
-    int ctas;
-    // CTAs of each list, and of each head's last list (which may hold one tile only and then needs fewer);
-    // no range crosses from one list to the next. per_last 0: all lists, laid end to end, are cut into
-    // `ctas` ranges.
-    int per_list, per_last;
-    __host__ __device__ int per_head() const { return (tile_pairs - 1) * per_list + per_last; }
-    double us;              // what the kernel is expected to take
+    int grid;               // blocks for prefix and suffixes together
+    float suffix_unit_us;   // an SM's time for one unit of the suffixes
+    FastDiv by_heads;
+    FastDiv by_share;       // a head's blocks (odd: ten times) to those of one full list
 };
-// `ctas`: the most to launch.
-PrefixPlan prefix_plan(int B, int Hq, int Hkv, int max_prefix_len, int ctas);
+// How one call divides the grid.
+struct PrefixSplit {
+    int ctas;                // blocks of the prefix
+    int per_list, per_last;  // of each list, and of a head's last list; per_last 0: cut end to end
+    __host__ __device__ int per_head(int tile_pairs) const { return (tile_pairs - 1) * per_list + per_last; }
+};
+PrefixPlan prefix_plan(int B, int Hq, int Hkv, int sm_count);
+// The split for a prefix of `tiles` KV tiles and suffixes of `work` units in all, the
+// pairs' own included; what it takes in us.
+double prefix_split(const PrefixPlan &plan, long long tiles, long long work, PrefixSplit *split);
+constexpr double kFixedSplitUs = 24.0;  // see prefix_split.cuh
 struct PrefixArgs {
     const void *q, *k_pages, *v_pages;
     const int *prefix_table, *prefix_len;  // [prefix_pages], [1]
-    int B, Hq, Hkv, num_pages, page_size, prefix_pages, max_prefix_len;
+    int B, Hq, Hkv, num_pages, page_size, prefix_pages, cap;  // cap: most keys of the prefix
     float scale;
     PrefixPlan plan;
+    PrefixSplit fixed;
+    PrefixSplit *split;  // null: `fixed`; otherwise worked out on the device and left here
     float *part_o, *part_lse;
     int *status;
 };
@@ -204,8 +210,12 @@ struct PrefixArgs {
 // pair are at pieces + (2 worker + (0 or 1)) * suffix_piece(heads_per_pair): O rows, then LSEs.
 constexpr int kSuffixWarps = 12;      // workers of a CTA
 constexpr int kSuffixUnitKeys = 16;
+// Ranges are cut by units and so many more for each pair: what its start and end cost the worker. (16,884
+// units of uneven suffixes on 34 SMs, their prefix on the others: 69.7 us without, 58.3, 58.1, 58.1 with 1, 2
+// and 4; 100 suffixes of 300 keys at most 17.4, 16.7, 16.9 and 17.8.)
+constexpr int kSuffixPairUnits = 2;
 constexpr int kSuffixMinUnits = 2;    // units a worker has at least, while there are fewer than workers
-// Workers that share `total` units in a grid of `ctas`.
+// Workers that share `total` units, the pairs' own included, in a grid of `ctas`.
 __host__ __device__ inline int suffix_workers(int total, int ctas)
 {
     const int want = (total + kSuffixMinUnits - 1) / kSuffixMinUnits, most = ctas * kSuffixWarps;
@@ -215,10 +225,8 @@ __host__ __device__ inline int suffix_workers(int total, int ctas)
 __host__ __device__ inline int suffix_piece(int heads_per_pair) { return heads_per_pair * 128 + (heads_per_pair + 3) / 4 * 4; }
 struct SuffixPlan {
     int heads_per_pair, head_groups;
-    long long units;  // at most: the lengths are read on the device
-    int ctas;
 };
-SuffixPlan suffix_plan(int B, int Hq, int Hkv, int max_seq_len, int ctas);
+SuffixPlan suffix_plan(int Hq, int Hkv);
 struct SuffixArgs {
     const void *q, *k_pages, *v_pages;
     const int *seq_lens, *block_table;
@@ -234,6 +242,8 @@ cudaError_t launch_prefix_decode(const PrefixArgs &a, const SuffixArgs *own, cud
 // Joins the prefix's segments and the suffixes' results into o (bf16) and lse (natural log).
 struct PrefixMergeArgs {
     PrefixPlan plan;
+    PrefixSplit fixed;
+    const PrefixSplit *split;  // as PrefixArgs
     int B, Hq, Hkv, cap;
     const int *prefix_len;
     const float *part_o, *part_lse;
@@ -243,7 +253,7 @@ struct PrefixMergeArgs {
     int suffix_cap;
     void *o;
     float *lse;
-    FastDiv by_hq, by_tile_seqs, by_tile_group, by_group, by_pair, by_ctas;  // set by launch_prefix_merge
+    FastDiv by_hq, by_tile_seqs, by_tile_group, by_group, by_pair;  // set by launch_prefix_merge
 };
 cudaError_t launch_prefix_merge(const PrefixMergeArgs &a, cudaStream_t stream);
 

@@ -22,6 +22,7 @@
 #include <cstdint>
 
 #include "kernels.h"
+#include "prefix_split.cuh"
 
 namespace attn_b200 {
 namespace {
@@ -100,13 +101,12 @@ namespace {
 
 // Attention of one row of a shared-prefix decode from its parts, all fp32 with LSEs in log2 units: the
 // segments of its list of prefix tiles (prefill_sm100.cu, decode_segment) and its suffix, whole or in
-// the pieces that the workers which shared its pair left (suffix_sm100.cu).
+// the pieces that the workers which shared its pair left (suffix_sm100.cuh).
 //   M = max LSE_s,  O = sum 2^(LSE_s - M) O_s / W,  lse = (M + log2 W) ln 2,  W = sum 2^(LSE_s - M).
 // kSplit warps take one row, each every kSplit-th part: lane i looks up where its i-th part lies and
 // its LSE (before any O is read), then each lane adds its four channels over the warp's parts, eight reads
 // in flight, and the warps' sums are joined in shared memory. Bound by the latency of that chain for few
-// rows (four warps a row: see the launch), by reading the parts, still in L2, for many. Where the parts lie follows from the lengths alone and is computed before the wait for
-// the kernels that write them. A row with no part (no prefix, no suffix) gives O = 0 and lse = -inf.
+// rows (four warps a row: see the launch), by reading the parts, still in L2, for many. Where the parts lie follows from the lengths and the split. A row with no part (no prefix, no suffix) gives O = 0 and lse = -inf.
 constexpr int kMergeWarps = 4;
 constexpr int kMergeSplitRows = 1024;
 
@@ -121,51 +121,51 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const Pr
         return;
     const int b = a.by_hq.quot(row), h = row - b * a.Hq;
 
-    // Prefix: the CTAs from the one that holds the list's first unit to the one that holds its last.
-    const int tile = a.by_tile_seqs.quot(b), part_of_heads = a.by_tile_group.quot(h);
-    const int in_tile = (b - tile * a.plan.tile_seqs) * a.plan.group + h - part_of_heads * a.plan.group;
-    const int list = part_of_heads * a.plan.tile_pairs + tile / 2;
     const int tiles = (min(max(__ldg(a.prefix_len), 0), a.cap) + kTile - 1) / kTile;
-    int c0 = 0, n_prefix = 0;
-    if (a.plan.per_last > 0) {
-        const int pair = tile / 2;
-        c0 = part_of_heads * a.plan.per_head() + pair * a.plan.per_list;
-        n_prefix = min(pair + 1 == a.plan.tile_pairs ? a.plan.per_last : a.plan.per_list, tiles);
-    } else if (tiles > 0) {
-        const EvenRange range(static_cast<unsigned>(a.plan.lists) * tiles, a.by_ctas);
-        c0 = static_cast<int>(range.part_of(list * tiles));
-        n_prefix = static_cast<int>(range.part_of((list + 1) * tiles - 1)) - c0 + 1;
-    }
-    // Suffix: its pair's units among all pairs' units, as suffix_kernel lays them.
-    int s0 = 0, n_suffix = 0, in_pair = 0, first_piece = 0;
+    const int per = a.suffix.heads_per_pair, pairs = a.Hkv * a.suffix.head_groups;
+    int before = 0, all = 0, own = 0;  // work of the sequences before b and of all, units of b
     if (a.o_suffix) {
-        const int group = a.by_group.d, per = a.suffix.heads_per_pair, pairs = a.Hkv * a.suffix.head_groups;
-        auto units_of = [&](int i) {
-            return (min(max(__ldg(a.seq_lens + i), 0), a.suffix_cap) + kSuffixUnitKeys - 1) / kSuffixUnitKeys;
-        };
-        int before = 0, all = 0;
+        own = suffix_units(__ldg(a.seq_lens + b), a.suffix_cap);
         for (int i = lane; i < a.B; i += 32) {
-            const int u = units_of(i);
+            const int u = suffix_work(__ldg(a.seq_lens + i), a.suffix_cap);
             all += u;
             before += i < b ? u : 0;
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            all += __shfl_xor_sync(0xffffffffu, all, o);
-            before += __shfl_xor_sync(0xffffffffu, before, o);
-        }
-        const int units = units_of(b), g = a.by_group.quot(h), in_group = h - g * group;
-        const int pair = a.by_pair.quot(in_group);
-        in_pair = in_group - pair * per;
-        if (units > 0) {
-            const int total = all * pairs;
-            const int first = before * pairs + (g * a.suffix.head_groups + pair) * units;
-            const EvenRange range(total, suffix_workers(total, a.suffix.ctas));
-            s0 = static_cast<int>(range.part_of(first));
-            n_suffix = static_cast<int>(range.part_of(first + units - 1)) - s0 + 1;
-            // The first worker's piece is its last one unless its range starts with the pair.
-            first_piece = static_cast<int>(range.begin(s0)) >= first ? 0 : 1;
-        }
+        before = __reduce_add_sync(0xffffffffu, before);
+        all = __reduce_add_sync(0xffffffffu, all);
+    }
+    const int total = all * pairs;
+    PrefixSplit split = a.fixed;
+    if (a.split) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        split.ctas = __ldcg(&a.split->ctas);
+        split.per_list = __ldcg(&a.split->per_list);
+        split.per_last = __ldcg(&a.split->per_last);
+    }
+    // Prefix: the blocks from the one that holds the list's first KV tile to the one that holds its last.
+    const int tile = a.by_tile_seqs.quot(b), part_of_heads = a.by_tile_group.quot(h);
+    const int in_tile = (b - tile * a.plan.tile_seqs) * a.plan.group + h - part_of_heads * a.plan.group;
+    const int pair = tile / 2, list = part_of_heads * a.plan.tile_pairs + pair;
+    int c0 = 0, n_prefix = 0;
+    if (split.per_last > 0) {
+        c0 = part_of_heads * split.per_head(a.plan.tile_pairs) + pair * split.per_list;
+        n_prefix = min(pair + 1 == a.plan.tile_pairs ? split.per_last : split.per_list, tiles);
+    } else if (tiles > 0) {
+        const EvenRange range(static_cast<unsigned>(a.plan.lists) * tiles, split.ctas);
+        c0 = static_cast<int>(range.part_of(list * tiles));
+        n_prefix = static_cast<int>(range.part_of((list + 1) * tiles - 1)) - c0 + 1;
+    }
+    // Suffix: its pair's units among all pairs' units, as suffix::run lays them.
+    int s0 = 0, n_suffix = 0, in_pair = 0, first_piece = 0;
+    if (own > 0) {
+        const int g = a.by_group.quot(h), in_group = h - g * static_cast<int>(a.by_group.d), hg = a.by_pair.quot(in_group);
+        in_pair = in_group - hg * per;
+        const int start = before * pairs + (g * a.suffix.head_groups + hg) * (own + kSuffixPairUnits), first = start + kSuffixPairUnits;
+        const EvenRange range(total, suffix_workers(total, a.plan.grid - split.ctas));
+        s0 = static_cast<int>(range.part_of(first));
+        n_suffix = static_cast<int>(range.part_of(first + own - 1)) - s0 + 1;
+        // The first worker's piece is its last one unless its range starts with the pair.
+        first_piece = static_cast<int>(range.begin(s0)) >= start ? 0 : 1;
     }
     const int n = n_prefix + n_suffix;
 
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const Pr
             *o = a.o_suffix + static_cast<size_t>(row) * D;
             *lse = a.lse_suffix + row;
         } else if (k < n) {
-            const int i = k - n_prefix, per = a.suffix.heads_per_pair;
+            const int i = k - n_prefix;
             const float *piece = a.pieces + (static_cast<size_t>(s0 + i) * 2 + (i == 0 ? first_piece : 0)) * suffix_piece(per);
             *o = piece + in_pair * D;
             *lse = piece + per * D + in_pair;
@@ -285,7 +285,6 @@ cudaError_t launch_prefix_merge(const PrefixMergeArgs &args, cudaStream_t stream
     a.by_tile_group = FastDiv(a.plan.group);
     a.by_group = FastDiv(a.Hq / a.Hkv);
     a.by_pair = FastDiv(a.suffix.heads_per_pair);
-    a.by_ctas = FastDiv(a.plan.ctas);
     static_assert(32 * kMergeWarps == 128, "one thread a channel");
     const int rows = a.B * a.Hq;
     // Up to a block an SM's worth of rows or so, latency counts; beyond it, the work a row costs.

@@ -53,13 +53,13 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
-#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <mutex>
 
 #include "kernels.h"
 #include "sm100_ptx.cuh"
+#include "prefix_split.cuh"
 #include "suffix_sm100.cuh"
 #include "tma_host.h"
 
@@ -143,16 +143,12 @@ struct Params {
     // their KV-tile count at the start of the kernel (the lengths are known on the device only).
     int sorted = 0;
     // Shared prefix of a decode: one new token per sequence, rows = (sequence, query head of the kv
-    // head's group) packed into tiles of tile_seqs sequences. block_table is the prefix's one row,
+    // head's group) packed into tiles of prefix.tile_seqs sequences. block_table is the prefix's one row,
     // seq_lens its one length; O and LSE leave as fp32 partials, 256 rows for each segment.
-    int heads = 0;      // kv heads times sub_groups
-    int sub_groups = 1; // equal parts of a kv head's group of more than 128 query heads; group is one part
-    int tile_seqs = 0;  // sequences in a 128-row tile
-    int tile_pairs = 0; // pairs of tiles per head: heads * tile_pairs lists of KV tiles
+    PrefixPlan prefix{};
+    PrefixSplit fixed{}, *split = nullptr;  // as PrefixArgs
     float *part_o = nullptr;    // [segment slot][256][128]
     float *part_lse = nullptr;  // [segment slot][256], log2 units
-    int ctas = 0;               // blocks that work on the prefix, the grid's first
-    int per_list = 0, per_last = 0;  // of them for each list (PrefixPlan)
 };
 
 // What an instantiation of the kernel computes: attention over a dense cache, over a paged,
@@ -271,41 +267,43 @@ struct Item {
 // ---- shared prefix of a decode ------------------------------------------------------------------
 // For each head and pair of tiles there is a list of all KV tiles of the prefix. The lists are cut into
 // ranges, one per CTA, whose lengths differ by one at most (EvenRange), so that a few rows still use every
-// SM: each list by itself, or all of them laid end to end (PrefixPlan says which). A CTA's part of one list is a segment: an item whose unnormalised softmax is
-// finished here and whose rows are merged with the list's other segments, and with the sequences' own
-// keys, by prefix_merge_kernel. Segment (list, CTA) has slot list + CTA: both grow along the lists, and
-// one of them does from each segment to the next, so slots are distinct and below lists + CTAs.
+// SM: each list by itself, or all of them laid end to end (split_prefix). A CTA's part of one list is a
+// segment: an item whose unnormalised softmax is finished here and whose rows are merged with the list's
+// other segments, and with the sequences' own keys, by prefix_merge_kernel. Segment (list, CTA) has slot
+// list + CTA: both grow along the lists, and one of them does from each segment to the next, so slots are
+// distinct and below lists + CTAs.
 
 __device__ __forceinline__ int prefix_length(const Params &p) { return min(max(__ldg(p.seq_lens), 0), p.cap); }
 
-// Segments of this CTA, worked out once (s_segments): list and range of the r-th are plain arithmetic.
+// Segments of this CTA, worked out once: list and range of the r-th are plain arithmetic.
 struct Segments {
     int len, tiles;       // the prefix's keys and KV tiles
     int begin, end;       // this CTA's range
     int first_list;       // list that holds `begin`
 };
+__shared__ PrefixSplit s_split;  // when it is worked out here
 __shared__ Segments s_segments;
 
-__device__ __forceinline__ Segments find_segments(const Params &p)
+__device__ __forceinline__ Segments find_segments(const Params &p, const PrefixSplit &split, int len)
 {
     Segments sg;
-    sg.len = prefix_length(p);
-    sg.tiles = (sg.len + kBN - 1) / kBN;
-    if (p.per_last > 0) {
-        const int per_head = (p.tile_pairs - 1) * p.per_list + p.per_last;
-        const int head = static_cast<int>(blockIdx.x) / per_head;
-        int i = static_cast<int>(blockIdx.x) - head * per_head;
-        const int pair = p.tile_pairs > 1 ? min(i / p.per_list, p.tile_pairs - 1) : 0;
-        i -= pair * p.per_list;
-        const int list = head * p.tile_pairs + pair;
-        const EvenRange r(sg.tiles, pair + 1 == p.tile_pairs ? p.per_last : p.per_list);
+    sg.len = len;
+    sg.tiles = (len + kBN - 1) / kBN;
+    const int cta = static_cast<int>(blockIdx.x), pairs = p.prefix.tile_pairs;
+    if (split.per_last > 0) {
+        const int per_head = split.per_head(pairs), head = cta / per_head;
+        int i = cta - head * per_head;
+        const int pair = pairs > 1 ? min(i / split.per_list, pairs - 1) : 0;
+        i -= pair * split.per_list;
+        const int list = head * pairs + pair;
+        const EvenRange r(sg.tiles, pair + 1 == pairs ? split.per_last : split.per_list);
         sg.begin = list * sg.tiles + static_cast<int>(r.begin(i));
         sg.end = list * sg.tiles + static_cast<int>(r.begin(i + 1));
         sg.first_list = list;
     } else {
-        const EvenRange r(static_cast<uint32_t>(p.heads) * p.tile_pairs * sg.tiles, static_cast<uint32_t>(p.ctas));
-        sg.begin = static_cast<int>(r.begin(blockIdx.x));
-        sg.end = static_cast<int>(r.begin(blockIdx.x + 1));
+        const EvenRange r(static_cast<uint32_t>(p.prefix.lists) * sg.tiles, static_cast<uint32_t>(split.ctas));
+        sg.begin = static_cast<int>(r.begin(cta));
+        sg.end = static_cast<int>(r.begin(cta + 1));
         sg.first_list = sg.tiles ? sg.begin / sg.tiles : 0;
     }
     return sg;
@@ -329,10 +327,10 @@ __device__ __forceinline__ Item decode_segment(const Params &p, int list)
     const int first = list * sg.tiles;
     it.kt0 = max(sg.begin - first, 0);
     const int n = min(sg.end - first, sg.tiles) - it.kt0;
-    it.kvh = list / p.tile_pairs;
-    const int pair = list - it.kvh * p.tile_pairs;
-    it.q0[0] = 2 * pair * p.tile_seqs;
-    it.q0[1] = it.q0[0] + p.tile_seqs;
+    it.kvh = list / p.prefix.tile_pairs;
+    const int pair = list - it.kvh * p.prefix.tile_pairs;
+    it.q0[0] = 2 * pair * p.prefix.tile_seqs;
+    it.q0[1] = it.q0[0] + p.prefix.tile_seqs;
     it.hq[0] = it.hq[1] = it.kvh;
     it.n[0] = n;
     it.n[1] = it.q0[1] < p.B ? n : 0;
@@ -465,14 +463,14 @@ __device__ __forceinline__ void run_tiles(const CUtensorMap &tm_q, const CUtenso
     }
     if constexpr (kMode == kPrefix) {
         // The rows behind a tile's last sequence are no TMA box's: zeros, so that their scores are finite.
-        const int used = p.tile_seqs * p.group;
+        const int used = p.prefix.tile_seqs * p.group;
         for (int i = threadIdx.x; i < 2 * C::kChunks * (kBM - used) * 8; i += kThreads) {
             const int u = i & 7, row = used + (i >> 3) % (kBM - used), c = (i >> 3) / (kBM - used);
             *reinterpret_cast<uint4 *>(smem + C::kOffQ + c * C::kChunkBytes + row * 128 + u * 16) = make_uint4(0u, 0u, 0u, 0u);
         }
         fence_proxy_async_smem();
         if (warp == 11 && lane == 0)
-            s_segments = find_segments(p);
+            s_segments = find_segments(p, p.split ? s_split : p.fixed, prefix_length(p));
     }
     if (warp == kWarpTma && lane == 0) {
         tma_prefetch_desc(&tm_q);
@@ -522,7 +520,7 @@ __device__ __forceinline__ void run_tiles(const CUtensorMap &tm_q, const CUtenso
                 // (sequence, head) of tile_seqs sequences one behind the other; zeros behind the batch.
                 if (issuer) {
                     mbar_arrive_expect_tx(BAR(kBarQFull), kMode == kPrefix
-                                                              ? n_q * C::kChunks * p.tile_seqs * p.group * C::kSwizzleBytes
+                                                              ? n_q * C::kChunks * p.prefix.tile_seqs * p.group * C::kSwizzleBytes
                                                               : n_q * C::kTileBytes);
 #pragma unroll
                     for (int x = 0; x < 2; ++x)
@@ -535,7 +533,7 @@ __device__ __forceinline__ void run_tiles(const CUtensorMap &tm_q, const CUtenso
                 }
                 ++q_issued;
                 const int n_loads = 2 * it.n_max();  // K0, V0, K1, V1, ...
-                const int kvh = kMode == kPrefix ? it.kvh / p.sub_groups : it.kvh;
+                const int kvh = kMode == kPrefix ? it.kvh / p.prefix.sub_groups : it.kvh;
                 // This lane's box of the current tile: first key, block-table entry, first slot in the page.
                 int key = 0, entry = 0, in_page = 0, page = 0;
                 auto look_up = [&]() {
@@ -989,7 +987,7 @@ __device__ __forceinline__ void run_tiles(const CUtensorMap &tm_q, const CUtenso
                 const int row0 = (cur.slot * 2 + x) * kBM + 32 * (warp & 3);
                 const int rr = lane >> 3, uu = lane & 7;
                 float *dst = p.part_o + static_cast<size_t>(row0 + rr) * D + 4 * uu;
-                const int rows = min(p.tile_seqs, p.B - q0) * p.group - 32 * (warp & 3);  // of this warp's 32
+                const int rows = min(p.prefix.tile_seqs, p.B - q0) * p.group - 32 * (warp & 3);  // of this warp's 32
 #pragma unroll 1  // once a segment: less code to fetch counts for more (unrolled it took 0.5 us longer)
                 for (int h = 0; h < (rows > 0 ? D / 32 : 0); ++h, dst += 32) {
                     uint32_t ov[32];
@@ -1099,8 +1097,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     run_tiles<D, kMode>(tm_q, tm_k, tm_v, tm_o, p, smem_raw);
 }
 
-// Decode over a shared prefix: the first p.ctas blocks take the prefix, the rest the suffixes. One launch,
-// because neither needs the other, and the merge behind it then waits for one grid.
+// Decode over a shared prefix: the grid's first blocks take the prefix, the rest the suffixes, as
+// split_prefix divides them. One launch, because neither needs the other, and the merge behind it then
+// waits for one grid. (No suffixes: sp.seq_lens is null.)
 template <int kGroups>
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -1110,11 +1109,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     static_assert(kThreads == 32 * kSuffixWarps, "one block size");
     extern __shared__ uint8_t smem_raw[];
     asm volatile("griddepcontrol.launch_dependents;");  // the merge, which waits for this grid's end
-    if (static_cast<int>(blockIdx.x) < p.ctas)
+    const int cta = static_cast<int>(blockIdx.x);
+    int ctas = p.fixed.ctas;
+    if (p.split) {
+        if (threadIdx.x < 32) {
+            const int lane = static_cast<int>(threadIdx.x), tiles = (prefix_length(p) + kBN - 1) / kBN;
+            int work = 0;
+            if (sp.seq_lens) {
+                for (int b = lane; b < p.B; b += 32)
+                    work += suffix_work(__ldg(sp.seq_lens + b), sp.cap);
+                work = __reduce_add_sync(0xffffffffu, work) * sp.Hkv * sp.head_groups;
+            }
+            const PrefixSplit split = split_prefix(p.prefix, tiles, work, lane);
+            if (lane == 0) {
+                s_split = split;
+                if (cta == 0)
+                    *p.split = split;
+            }
+        }
+        __syncthreads();
+        ctas = s_split.ctas;
+    }
+    if (cta < ctas)
         run_tiles<128, kPrefix>(tm_q, tm_k, tm_v, tm_q, p, smem_raw);
-    else
-        suffix::run<kGroups>(tm_sk, tm_sv, sp, smem_raw, static_cast<int>(blockIdx.x) - p.ctas,
-                             static_cast<int>(gridDim.x) - p.ctas);
+    else if (sp.seq_lens)
+        suffix::run<kGroups>(tm_sk, tm_sv, sp, smem_raw, cta - ctas, static_cast<int>(gridDim.x) - ctas);
 }
 
 // Sets a kernel's attributes on the current device once (`set`: its flags, by device; benign race
@@ -1242,7 +1261,7 @@ cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream, int *encod
     }
 }
 
-PrefixPlan prefix_plan(int B, int Hq, int Hkv, int max_prefix_len, int ctas)
+PrefixPlan prefix_plan(int B, int Hq, int Hkv, int sm_count)
 {
     PrefixPlan pl;
     // A tile holds whole groups of query heads; a group above 128 heads goes in equal parts.
@@ -1251,50 +1270,41 @@ PrefixPlan prefix_plan(int B, int Hq, int Hkv, int max_prefix_len, int ctas)
         ++sub;
     pl.sub_groups = sub;
     pl.group = group / sub;
+    pl.heads = Hkv * sub;
     pl.tile_seqs = kBM / pl.group;
     const int tiles = (B + pl.tile_seqs - 1) / pl.tile_seqs;
     pl.tile_pairs = (tiles + 1) / 2;
-    pl.lists = static_cast<long long>(Hkv) * sub * pl.tile_pairs;
-    pl.units = pl.lists * ((static_cast<long long>(max_prefix_len) + kBN - 1) / kBN);
-    // A KV tile takes 2.0 us of an SM, 1.6 us in a list of one query tile; a segment's start and end 4.5 us
-    // for the first of a CTA and 2 us for another. Cutting each list by itself gives every CTA one segment
-    // but may leave SMs without work; cutting all lists as one gives most CTAs two. Whichever ends first.
-    const long long tiles_kv = (static_cast<long long>(max_prefix_len) + kBN - 1) / kBN;
-    const double full_us = 2.0, last_us = tiles % 2 ? 1.6 : 2.0;
-    auto up = [](long long n, long long d) { return (n + d - 1) / d; };
-    pl.per_list = pl.per_last = 0;
-    pl.ctas = static_cast<int>(pl.units < 1 ? 1 : pl.units < ctas ? pl.units : ctas);
-    pl.us = 4.5 + full_us * static_cast<double>(up(pl.units, pl.ctas)) + 2.0;
-    const long long heads = static_cast<long long>(Hkv) * sub, each = ctas / heads;  // CTAs for one head
-    for (long long per = pl.tile_pairs > 1 ? 1 : 0; tiles_kv > 0 && (pl.tile_pairs - 1) * per < each; ++per) {
-        long long last = std::min(each - (pl.tile_pairs - 1) * per, tiles_kv);
-        const double us_full = per ? full_us * static_cast<double>(up(tiles_kv, per)) : 0.0;
-        const double us = 4.5 + std::max(us_full, last_us * static_cast<double>(up(tiles_kv, last)));
-        if (us < pl.us) {
-            last = up(tiles_kv, up(tiles_kv, last));  // no more CTAs than that time takes
-            pl.us = us;
-            pl.per_list = static_cast<int>(per);
-            pl.per_last = static_cast<int>(last);
-            pl.ctas = static_cast<int>(heads * pl.per_head());
-        }
-        if (pl.tile_pairs == 1 || per >= tiles_kv)
-            break;
-    }
+    pl.odd = tiles % 2;
+    pl.lists = static_cast<long long>(pl.heads) * pl.tile_pairs;
+    pl.grid = sm_count > 2 ? sm_count : 2;  // one block for each part at least
+    pl.suffix_unit_us = Hq / Hkv > 8 ? 0.098f : 0.074f;
+    pl.by_heads = FastDiv(pl.heads);
+    pl.by_share = FastDiv(pl.odd ? 10 * (pl.tile_pairs - 1) + 8 : pl.tile_pairs);
     return pl;
 }
 
-SuffixPlan suffix_plan(int B, int Hq, int Hkv, int max_seq_len, int ctas)
+double prefix_split(const PrefixPlan &plan, long long tiles, long long work, PrefixSplit *split)
 {
-    SuffixPlan pl;
+    *split = PrefixSplit{};
+    if (tiles == 0)
+        return 0.0;
+    float best = INFINITY;
+    const int n = split_candidates(plan);
+    for (int i = 0; i < n; ++i) {
+        PrefixSplit s;
+        const float us = split_candidate(plan, i, static_cast<float>(tiles), static_cast<float>(work), &s);
+        if (us < best) {
+            best = us;
+            *split = s;
+        }
+    }
+    return best;
+}
+
+SuffixPlan suffix_plan(int Hq, int Hkv)
+{
     const int group = Hq / Hkv;
-    pl.heads_per_pair = group < 16 ? group : 16;
-    pl.head_groups = (group + 15) / 16;
-    pl.units = static_cast<long long>(B) * Hkv * pl.head_groups * ((static_cast<long long>(max_seq_len) + kSuffixUnitKeys - 1) / kSuffixUnitKeys);
-    // As many CTAs as the workers there can be at most need, so that the others' SMs are free for the
-    // prefix.
-    const long long want = (pl.units + kSuffixMinUnits - 1) / kSuffixMinUnits;
-    pl.ctas = static_cast<int>(want < 1 ? 1 : want < ctas ? want : ctas);
-    return pl;
+    return SuffixPlan{group < 16 ? group : 16, (group + 15) / 16};
 }
 
 cudaError_t launch_prefix_decode(const PrefixArgs &a, const SuffixArgs *own, cudaStream_t stream, int *encode_error)
@@ -1346,30 +1356,25 @@ cudaError_t launch_prefix_decode(const PrefixArgs &a, const SuffixArgs *own, cud
     p.Hkv = a.Hkv;
     p.Sq = 1;
     p.group = pl.group;
-    p.sub_groups = pl.sub_groups;
-    p.heads = a.Hkv * pl.sub_groups;
-    p.tile_seqs = pl.tile_seqs;
-    p.tile_pairs = pl.tile_pairs;
+    p.prefix = pl;
+    p.fixed = a.fixed;
+    p.split = a.split;
     p.scale_log2 = a.scale * kLog2e;
     p.seq_lens = a.prefix_len;
     p.block_table = a.prefix_table;
     p.num_pages = a.num_pages;
     p.page_size = a.page_size;
     p.pages_per_seq = a.prefix_pages;
-    const long long cap = static_cast<long long>(a.prefix_pages) * a.page_size;
-    p.cap = static_cast<int>(cap < a.max_prefix_len ? cap : a.max_prefix_len);
+    p.cap = a.cap;
     p.part_o = a.part_o;
     p.part_lse = a.part_lse;
-    p.ctas = pl.ctas;
-    p.per_list = pl.per_list;
-    p.per_last = pl.per_last;
     constexpr int kSmem = C::kSmem > suffix::kSmem ? C::kSmem : suffix::kSmem;
     static bool set[2][kMaxDevices] = {};
     auto launch = [&](auto kernel, bool (&done)[kMaxDevices]) {
         const cudaError_t ready = prepare(kernel, kSmem, done);
         if (ready != cudaSuccess)
             return ready;
-        kernel<<<static_cast<unsigned>(pl.ctas + (own ? own->plan.ctas : 0)), kThreads, kSmem, stream>>>(tq, tk, tv, tsk, tsv, p, sp);
+        kernel<<<static_cast<unsigned>(pl.grid), kThreads, kSmem, stream>>>(tq, tk, tv, tsk, tsv, p, sp);
         return cudaGetLastError();
     };
     return own && own->plan.heads_per_pair > 8 ? launch(prefix_decode_kernel<2>, set[1]) : launch(prefix_decode_kernel<1>, set[0]);

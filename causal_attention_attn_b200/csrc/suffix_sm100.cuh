@@ -5,8 +5,8 @@
  *
  * What it has to do is read every suffix's K and V once; the suffixes are many, short and of different
  * lengths. So the worker is one warp, not a CTA: a pair is one (sequence, kv head, up to 16 of its query
- * heads), its keys are units of 16, all pairs' units are laid end to end and cut evenly over the warps
- * of the grid (EvenRange). Each warp streams its units through a ring of its own by TMA and no warp
+ * heads), its keys are units of 16, all pairs' units are laid end to end, two more before each pair for
+ * what its start and end cost a warp, and cut evenly over the warps of the grid (EvenRange). Each warp streams its units through a ring of its own by TMA and no warp
  * waits for another, so the start and the end of a pair are hidden behind the other eleven warps of the
  * SM. (The CTA-wide paged decode kernel, whose 128-key chunks pass through one softmax, took 53 us where
  * this takes 31, for 125 sequences of up to 768 keys and 6 kv heads: it drains at every pair.)
@@ -48,8 +48,9 @@ constexpr int kBoxBytes = kKeys * 128;        // 16 keys x 64 dims
 constexpr int kStageBytes = 4 * kBoxBytes;    // K dims 0-63, 64-127, then V
 constexpr int kOffBar = kWarps * kStages * kStageBytes;
 constexpr int kOffMisc = kOffBar + kWarps * kStages * 8;
-constexpr int kOffStart = kOffMisc + 16;                    // first unit of each sequence, and the total
-constexpr int kOffLen = kOffStart + 4 * (kPagedMaxBatch + 1);  // clamped lengths
+constexpr int kOffStart = kOffMisc + 16;                    // where each sequence starts, and the end of all
+constexpr int kOffUnits = kOffStart + 4 * (kPagedMaxBatch + 1);  // units before each sequence
+constexpr int kOffLen = kOffUnits + 4 * (kPagedMaxBatch + 1);    // clamped lengths
 constexpr int kSmem = kOffLen + 4 * kPagedMaxBatch + 1024;  // + alignment of the base
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
 constexpr float kRescaleThreshold = 8.0f;
@@ -115,7 +116,7 @@ __device__ __forceinline__ void run(const CUtensorMap &tm_k, const CUtensorMap &
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffMisc);
-    int *start = reinterpret_cast<int *>(smem + kOffStart), *len = reinterpret_cast<int *>(smem + kOffLen);
+    int *start = reinterpret_cast<int *>(smem + kOffStart), *before = reinterpret_cast<int *>(smem + kOffUnits), *len = reinterpret_cast<int *>(smem + kOffLen);
     const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(warp * kStages * kStageBytes);
     const uint32_t bar0 = smem_u32(smem) + kOffBar + static_cast<uint32_t>(warp * kStages * 8);
     const int pairs = p.Hkv * p.head_groups;  // of a sequence
@@ -132,23 +133,29 @@ __device__ __forceinline__ void run(const CUtensorMap &tm_k, const CUtensorMap &
     for (int b = threadIdx.x; b < p.B; b += 32 * kWarps)
         len[b] = min(max(__ldg(p.seq_lens + b), 0), p.cap);
     __syncthreads();
-    if (warp == 0) {  // exclusive sums of the sequences' units
-        int running = 0;
+    if (warp == 0) {  // exclusive sums of the sequences' units, with and without the pairs' own
+        int places = 0, units = 0;
         for (int base = 0; base < p.B; base += 32) {
             const int b = base + lane;
-            const int u = b < p.B ? pairs * ((len[b] + kKeys - 1) / kKeys) : 0;
-            int sum = u;
+            const int u = b < p.B ? pairs * ((len[b] + kKeys - 1) / kKeys) : 0, w = u > 0 ? u + pairs * kSuffixPairUnits : 0;
+            int sum_w = w, sum_u = u;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, sum, o);
-                sum += lane >= o ? y : 0;
+                const int y = __shfl_up_sync(0xffffffffu, sum_w, o), z = __shfl_up_sync(0xffffffffu, sum_u, o);
+                sum_w += lane >= o ? y : 0;
+                sum_u += lane >= o ? z : 0;
             }
-            if (b < p.B)
-                start[b] = running + sum - u;
-            running += __shfl_sync(0xffffffffu, sum, 31);
+            if (b < p.B) {
+                start[b] = places + sum_w - w;
+                before[b] = units + sum_u - u;
+            }
+            places += __shfl_sync(0xffffffffu, sum_w, 31);
+            units += __shfl_sync(0xffffffffu, sum_u, 31);
         }
-        if (lane == 0)
-            start[p.B] = running;
+        if (lane == 0) {
+            start[p.B] = places;
+            before[p.B] = units;
+        }
     }
     __syncthreads();
     const int total = start[p.B];
@@ -158,24 +165,34 @@ __device__ __forceinline__ void run(const CUtensorMap &tm_k, const CUtensorMap &
     if (worker >= workers)
         return;
     const EvenRange range(total, workers);
-    const int g0 = static_cast<int>(range.begin(worker)), n_units = static_cast<int>(range.begin(worker + 1)) - g0;
 
-    Cursor first;
-    {
-        int lo = 0, hi = p.B - 1;  // the last sequence that starts at or before g0: it has units
+    // The first unit at or behind a place: even lanes find the range's begin, odd lanes its end.
+    Cursor first{};
+    int g0 = before[p.B];
+    const int place = static_cast<int>(range.begin(worker + (lane & 1)));
+    if (place < total) {
+        int lo = 0, hi = p.B - 1;  // the last sequence that starts at or before it: it has units
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (start[mid] <= g0)
+            if (start[mid] <= place)
                 lo = mid;
             else
                 hi = mid - 1;
         }
         first.b = lo;
         first.units = (len[lo] + kKeys - 1) / kKeys;
-        const int w = g0 - start[lo];
-        first.pair = w / first.units;
-        first.unit = w - first.pair * first.units;
+        const int w = place - start[lo];
+        first.pair = w / (first.units + kSuffixPairUnits);
+        first.unit = max(w - first.pair * (first.units + kSuffixPairUnits) - kSuffixPairUnits, 0);
+        g0 = before[lo] + first.pair * first.units + first.unit;
     }
+    const int n_units = __shfl_sync(0xffffffffu, g0, 1) - __shfl_sync(0xffffffffu, g0, 0);
+    first.b = __shfl_sync(0xffffffffu, first.b, 0);
+    first.pair = __shfl_sync(0xffffffffu, first.pair, 0);
+    first.unit = __shfl_sync(0xffffffffu, first.unit, 0);
+    first.units = __shfl_sync(0xffffffffu, first.units, 0);
+    if (n_units == 0)
+        return;
     auto next_pair = [&](Cursor &c) {
         c.unit = 0;
         if (++c.pair == pairs) {

@@ -95,6 +95,31 @@ def test_matches_oracle(case):
         assert rep.ok(), f"sequence {b} (suffix {lens[b]}): {rep}"
 
 
+def widen(t, entries):
+    """A table with room for far more pages than there are; the entries behind the real ones name page 0."""
+    return torch.cat((t, t.new_zeros(t.shape[:-1] + (entries - t.shape[-1],))), dim=-1)
+
+
+@pytest.mark.parametrize("case", CASES + [
+    (150, 8, 2, 900, [0, 300, 1, 17, 0] * 30, 16),   # short and long suffixes side by side, and none
+    (40, 20, 1, 1500, [250, 3, 0, 90] * 10, 64),     # more than eight heads to a pair
+    (1, 8, 8, 9000, [5000], 128),
+    (9, 32, 8, 0, [40] * 9, 16),
+], ids=lambda c: "b{}_hq{}_hkv{}_p{}_page{}".format(*c[:4], c[5]))
+def test_lengths_far_below_the_bounds(case):
+    """Such a call's split between prefix and suffixes is worked out on the device, from its real lengths."""
+    B, Hq, Hkv, plen, lens, page = case
+    if isinstance(lens, int):
+        lens = [int(x) for x in np.random.RandomState(B).randint(0, lens + 1, size=B)]
+    q, pre, suf, pages, ptab, table = make(B, Hq, Hkv, plen, lens, page, seed=B + plen)
+    big = 4 << 20
+    o, lse = call(q, pages, widen(ptab, big // page), plen, widen(table, 65536 // page), lens, max_prefix_len=big,
+                  max_seq_len=65536)
+    for b in range(B):
+        rep = compare(o[b:b + 1], lse[b:b + 1], *expect(q, pre, suf, lens, b, D ** -0.5))
+        assert rep.ok(), f"sequence {b} (suffix {lens[b]}): {rep}"
+
+
 def test_empty_prefix_and_empty_sequences():
     B, Hq, Hkv, lens, page = 3, 8, 2, [70, 0, 5], 16
     q, pre, suf, pages, ptab, table = make(B, Hq, Hkv, 64, lens, page, seed=1)
