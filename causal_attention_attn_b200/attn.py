@@ -665,10 +665,9 @@ def attn_qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor | 
     _, dks = _rows("dk", dk, dev, kshape)
     dwq = dwk = ws = None
     if qw is not None:
-        # One block for the weights' gradients (rows of 16-byte aligned floats), one for the kernels.
-        dwq, dwk = q.new_empty((2, D), dtype=torch.float32).unbind(0)
+        dwq, dwk = q.new_empty((D,), dtype=torch.float32), q.new_empty((D,), dtype=torch.float32)
         ws = q.new_empty((_NORM_ROPE_BWD_BLOCKS * 2 * D,), dtype=torch.float32)
-        _used_on(stream, dwq, ws)
+        _used_on(stream, dwq, dwk, ws)
     _call(load_library().attn_qk_norm_rope_bwd, dev, stream, q.data_ptr(), k.data_ptr(), qw, kw, _ptr(cos), _ptr(sin), pos,
           dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), _ptr(dwq), _ptr(dwk), _ptr(ws), B, Hq, Hkv, S,
           D, qs, ks, dqos, dkos, dqs, dks, rot_dim, max_pos, 1 if interleaved else 0, eps)

@@ -102,12 +102,13 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendParams 
             a.i = tok - a.b * p.seq.d;
             const uint32_t base = ring + static_cast<uint32_t>(s * kStageBytes);
             const __nv_bfloat16 *x = sc.x + (a.b * sc.xs.b + a.h * sc.xs.h + a.i * sc.xs.s);
-            copy_row(base, x, le, a.live0);
-            copy_row(base + kRowSlots * kSlotBytes, a.live1 ? x + sc.xs.h : x, le, a.live1);
-            const long long S = p.seq.d;
-            const long long fresh = p.new_lens ? min(max(static_cast<long long>(__ldg(p.new_lens + a.b)), 0LL), S) : S;
+            const int S = static_cast<int>(p.seq.d);
+            // Rows of padding are not read. (Without new_lens the rows wait for no length.)
+            const bool fresh = !p.new_lens || static_cast<int>(a.i) >= S - min(max(__ldg(p.new_lens + a.b), 0), S);
+            copy_row(base, x, le, a.live0 && fresh);
+            copy_row(base + kRowSlots * kSlotBytes, a.live1 ? x + sc.xs.h : x, le, a.live1 && fresh);
             const long long place = static_cast<long long>(__ldg(p.seq_lens + a.b)) - S + a.i;
-            a.token = a.live0 && a.i >= S - fresh && place >= 0 && place < p.cap;
+            a.token = a.live0 && fresh && place >= 0 && place < p.cap;
             const int pos = p.positions ? __ldg(p.positions + tok) : static_cast<int>(a.token ? place : 0);
             a.token = a.token && p.table.has(pos);
             a.page = -1;
