@@ -437,7 +437,8 @@ int attn_qk_norm_rope_bwd(const void *q, const void *k, const void *q_weight, co
  * A row is left out when it is padding, when its place lies outside [0, pages_per_seq * page_size),
  * when its block-table entry lies outside [0, num_pages), or (rot_dim > 0) its position outside
  * [0, max_pos): nothing of the cache changes for it, and its q_out rows are zeros. Every other slot of
- * the cache stays as it was. Two tokens of one call that name the same slot leave either one's row.
+ * the cache stays as it was. Where two tokens of one call name the same slot, each 16 bytes (e4m3: 8) of
+ * it are one token's or the other's.
  * Lengths are read on the device. Never allocates or synchronises; errors as the calls above.
  */
 int attn_append_paged(const void *q, const void *k, const void *v, const void *q_weight, const void *k_weight,

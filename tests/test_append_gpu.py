@@ -142,6 +142,50 @@ def test_bad_table_entries_write_nothing(fp8):
     ref.within(got, expect[0], expect[1], "q_out")
 
 
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_two_tokens_of_one_slot(fp8):
+    """Two sequences that share a page: every 16 bytes (e4m3: 8) of the slot are one token's or the other's."""
+    B, Hkv, page = 2, 8, 16
+    qkv, w, pages, coef, table, cos, sin, g = make(B, 0, Hkv, 1, page, 1, 31, True, 128, fp8, max_pos=page)
+    k, v = qkv[:, :, :Hkv].transpose(1, 2).cuda(), qkv[:, :, Hkv:].transpose(1, 2).cuda()
+    fn = attn.attn_append_paged_fp8 if fp8 else attn.attn_append_paged
+    scales = [c.cuda() for c in coef] if fp8 else []
+    lens = torch.tensor([4, 4], dtype=torch.int32).cuda()
+
+    def append(tab):
+        kp, vp = pages[0].cuda(), pages[1].cuda()
+        fn(k, v, cos.cuda(), sin.cuda(), kp, vp, *scales, torch.tensor(tab, dtype=torch.int32).cuda(), lens, k_weight=w[1].cuda())
+        return kp.cpu(), vp.cpu()
+
+    apart, same = append([[0], [1]]), append([[1], [1]])
+    for one, two in zip(apart, same):
+        a, b, c = (t.contiguous().view(torch.uint8).view(Hkv, -1, 8 if fp8 else 16) for t in (one[0, :, 3], one[1, :, 3], two[1, :, 3]))
+        assert torch.all((c == a).all(-1) | (c == b).all(-1))
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_padding_may_hold_anything(fp8):
+    B, Hq, Hkv, Sq, page = 3, 4, 2, 12, 16
+    qkv, w, pages, coef, table, cos, sin, g = make(B, Hq, Hkv, Sq, page, 2, 32, True, 128, fp8, max_pos=32)
+    new = [5, 0, 12]
+    fn = attn.attn_append_paged_fp8 if fp8 else attn.attn_append_paged
+    scales = [c.cuda() for c in coef] if fp8 else []
+    res = []
+    for fill in (float("nan"), 1.0):
+        t = qkv.clone()
+        for b in range(B):
+            t[b, :Sq - new[b]] = fill
+        t = t.cuda()
+        q, k, v = (t[:, :, a:b].transpose(1, 2) for a, b in ((0, Hq), (Hq, Hq + Hkv), (Hq + Hkv, Hq + 2 * Hkv)))
+        kp, vp = pages[0].cuda(), pages[1].cuda()
+        q_out = fn(k, v, cos.cuda(), sin.cuda(), kp, vp, *scales, table.cuda(), torch.tensor([20, 12, 31], dtype=torch.int32).cuda(),
+                   q=q, q_weight=w[0].cuda(), k_weight=w[1].cuda(), new_lens=torch.tensor(new, dtype=torch.int32).cuda())
+        for b in range(B):
+            assert torch.all(q_out[b, :, :Sq - new[b]] == 0)
+        res.append([x.cpu().view(torch.uint8) for x in (q_out, kp, vp)])
+    assert all(torch.equal(a, b) for a, b in zip(*res))
+
+
 def test_e4m3_special_values():
     """NaN stays NaN, infinities and large values saturate, ties go to the even code."""
     k = torch.zeros((1, 1, 1, D), dtype=torch.bfloat16)
