@@ -6,9 +6,9 @@
  *
  * Row arithmetic as in norm_rope_sm100.cu. With an e4m3 cache a key or value element x is stored as
  * the code nearest to x / coefficient (ties to even, saturating at +-448), from the fp32 value: a key
- * is rounded once, not to bf16 first. The quotient is __fdividef's (within 2 units in the last place
- * for coefficients in [2^-126, 2^126]): only a quotient within 2^-22 of halfway between two codes can
- * take the other one, and exact division cost 18 us of 94 for 16384 tokens.
+ * is rounded once, not to bf16 first. The quotient is x times the coefficient's approximate reciprocal
+ * (within 2 units in the last place for coefficients in [2^-126, 2^126]): only a quotient within 2^-22 of
+ * halfway between two codes can take the other one, and exact division cost 18 us of 94 for 16384 tokens.
  *
  * Bound by memory (each new row read and written once), and for a few tokens by the launch and one
  * chain of dependent loads: length, block-table entry and angles, store. The persistent blocks and
@@ -61,12 +61,18 @@ constexpr int kAngles = 2 * kRowSlots;  // a stage: two rows, then the angles
 constexpr int kStageBytes = (kAngles + kAngleSlots) * kSlotBytes;
 constexpr int kSmem = kWarps * kStages * kStageBytes;
 
-// Four consecutive elements' e4m3 codes, the first in the low byte.
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
+// The e4m3 codes of x / c, as x times c's reciprocal, which the hardware gives to a unit in the last place.
+__device__ __forceinline__ float reciprocal(float c)
 {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
-    return lo | (hi << 16);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(c));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t quotient_codes(float x0, float x1, float c0, float c1)
+{
+    return __nv_cvt_float2_to_fp8x2(__fmul2_rn(make_float2(x0, x1), make_float2(reciprocal(c0), reciprocal(c1))), __NV_SATFINITE,
+                                    __NV_E4M3);
 }
 
 template <bool kInterleaved, bool kFp8>
@@ -186,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendParams 
                         const int e = 4 * j + t;  // of the lane's sixteen
                         v[t] = kInterleaved ? ((e & 1) ? x[k].B[e >> 1] : x[k].A[e >> 1]) : (e < 8 ? x[k].A[e & 7] : x[k].B[e & 7]);
                     }
-                    codes[j] = e4m3x4(__fdividef(v[0], f.x), __fdividef(v[1], f.y), __fdividef(v[2], f.z), __fdividef(v[3], f.w));
+                    codes[j] = quotient_codes(v[0], v[1], f.x, f.y) | (quotient_codes(v[2], v[3], f.z, f.w) << 16);  // the first in the low byte
                 }
                 uint8_t *out = static_cast<uint8_t *>(p.pages[kind - kK]) + dst + (k ? next_head : 0);
                 *reinterpret_cast<uint2 *>(out + le.e0) = make_uint2(codes[0], codes[1]);
