@@ -810,6 +810,12 @@ extern "C" int attn_decode_prefix(const void *q, const void *k_pages, const void
         static_cast<long long>(pages_per_seq) * page_size > INT_MAX ||
         static_cast<long long>(prefix_pages) * page_size > INT_MAX)
         return ATTN_ERR_SHAPE;
+    // Keys are numbered in 31 bits, and so is the end of the last KV tile.
+    const long long prefix_cap = std::min(static_cast<long long>(prefix_pages) * page_size,
+                                          static_cast<long long>(max_prefix_len));
+    const long long own_cap = std::min(static_cast<long long>(pages_per_seq) * page_size, static_cast<long long>(max_seq_len));
+    if (prefix_cap > INT_MAX - 127 || own_cap > INT_MAX - 127)
+        return ATTN_ERR_SHAPE;
     auto aligned4 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; };
     if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o) || !aligned16(lse) ||
         (reinterpret_cast<uintptr_t>(workspace) & 255u) || !aligned4(prefix_table) || !aligned4(prefix_len) ||
@@ -829,9 +835,6 @@ extern "C" int attn_decode_prefix(const void *q, const void *k_pages, const void
     if (workspace_bytes < static_cast<long long>(sp.bytes))
         return ATTN_ERR_WORKSPACE;
     // The prefix's units (KV tiles of all lists) and the suffixes' are numbered in 31 bits.
-    const long long prefix_cap = std::min(static_cast<long long>(prefix_pages) * page_size,
-                                          static_cast<long long>(max_prefix_len));
-    const long long own_cap = std::min(static_cast<long long>(pages_per_seq) * page_size, static_cast<long long>(max_seq_len));
     const long long own_pairs = static_cast<long long>(B) * Hkv * suffix.head_groups;
     if (pl.lists > INT_MAX / ((prefix_cap + 127) / 128 + 1) || own_pairs > INT_MAX / (own_cap / kSuffixUnitKeys + 1 + kSuffixPairUnits))
         return ATTN_ERR_SHAPE;

@@ -168,6 +168,7 @@ def prefix(lib, **kw):
     ("page size 80", dict(page=80), -2),
     ("pages past 32 bits", dict(num_pages=1 << 30), -2),
     ("prefix past 32 bits", dict(prefix_pages=1 << 26), -2),
+    ("last tile past 31 bits", dict(prefix_pages=(1 << 25) - 1, page=64, max_prefix=(1 << 31) - 1), -2),
     ("gqa not divisible", dict(Hq=7), -3),
     ("misaligned workspace", dict(ws=A[9] + 16), -5),
     ("misaligned lse", dict(lse=A[8] + 4), -5),
