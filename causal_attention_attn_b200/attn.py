@@ -597,7 +597,7 @@ def _positions(positions, B, S, dev):
 
 
 def _new_rows(like):
-    return torch.empty(like.shape, dtype=torch.bfloat16, device=like.device)
+    return torch.empty_like(like, memory_format=torch.contiguous_format)
 
 
 def _used_on(stream, *tensors):
@@ -790,8 +790,8 @@ def attn_decode_prefix(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Te
         raise ValueError("block_table and seq_lens need one row / entry per batch element, prefix_len one entry")
     if scale is None:
         scale = D ** -0.5
-    out = torch.empty(qshape, dtype=torch.bfloat16, device=q.device) if out is None else out
-    lse = torch.empty((B, Hq, 1), dtype=torch.float32, device=q.device) if lse is None else lse
+    out = torch.empty_like(q) if out is None else out
+    lse = q.new_empty((B, Hq, 1), dtype=torch.float32) if lse is None else lse
     if _flat("out", out, torch.bfloat16, 4, dev) != qshape or _flat("lse", lse, torch.float32, 3, dev) != (B, Hq, 1):
         raise ValueError(f"out must be {tuple(qshape)} and lse {(B, Hq, 1)}")
     if workspace is None:
