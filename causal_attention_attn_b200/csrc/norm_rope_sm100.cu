@@ -282,30 +282,41 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_kernel(const NormRopePa
     }
 }
 
-// dw[side][d] = the blocks' partials added up: one block per side and 32 channels, its 32 warps each
-// over every 32nd partial, then the warps' sums in order.
+// dw[side][d] = the blocks' partials added up: one block per side and 32 channels, eight lanes to a partial
+// (four channels each), 128 partials at a time; then the four partials of a warp and the warps' sums in order.
 __global__ void __launch_bounds__(1024) weight_grad_kernel(const float *partials, int blocks, int D, float *dwq, float *dwk)
 {
-    __shared__ float red[32][33];
+    __shared__ float4 red[32][8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int side = blockIdx.y, d = blockIdx.x * 32 + lane;
+    const int side = blockIdx.y, d0 = blockIdx.x * 32;
     float *dst = side ? dwk : dwq;
     // Launched while the gradient's last blocks still run (see the launch): their partials are complete
     // only behind this.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!dst)
         return;
-    float t = 0.f;
-    for (int b = warp; b < blocks; b += 32)
-        t += partials[(static_cast<size_t>(b) * 2 + side) * D + d];
-    red[warp][lane] = t;
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 5  // all of them at once: kNormRopeBwdBlocks / 128
+    for (int b = 4 * warp + (lane >> 3); b < blocks; b += 128) {
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(partials + (static_cast<size_t>(b) * 2 + side) * D + d0) + (lane & 7));
+        t.x += v.x, t.y += v.y, t.z += v.z, t.w += v.w;
+    }
+#pragma unroll
+    for (int o = 8; o < 32; o <<= 1) {
+        t.x += __shfl_xor_sync(0xffffffffu, t.x, o);
+        t.y += __shfl_xor_sync(0xffffffffu, t.y, o);
+        t.z += __shfl_xor_sync(0xffffffffu, t.z, o);
+        t.w += __shfl_xor_sync(0xffffffffu, t.w, o);
+    }
+    if (lane < 8)
+        red[warp][lane] = t;
     __syncthreads();
     if (warp == 0) {
-        t = 0.f;
+        float sum = 0.f;
 #pragma unroll
         for (int v = 0; v < 32; ++v)
-            t += red[v][lane];
-        dst[d] = t;
+            sum += reinterpret_cast<const float *>(red[v])[lane];
+        dst[d0 + lane] = sum;
     }
 }
 
