@@ -439,6 +439,8 @@ int attn_qk_norm_rope_bwd(const void *q, const void *k, const void *q_weight, co
  * [0, max_pos): nothing of the cache changes for it, and its q_out rows are zeros. Every other slot of
  * the cache stays as it was. Where two tokens of one call name the same slot, each 16 bytes (e4m3: 8) of
  * it are one token's or the other's.
+ * A dense cache [B, Hkv, S, 128] (attn_fwd's k and v; S a page size) is one of B pages of S keys:
+ * page_size S, block_table[b][0] = b.
  * Lengths are read on the device. Never allocates or synchronises; errors as the calls above.
  */
 int attn_append_paged(const void *q, const void *k, const void *v, const void *q_weight, const void *k_weight,

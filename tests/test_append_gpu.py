@@ -270,6 +270,27 @@ def test_decode_steps_through_a_graph(fp8):
             assert rep.lse_max_abs <= 1e-3 and rep.o_max_abs <= 1e-2 * max(1.0, float(vv.float().abs().max())), rep
 
 
+def test_a_dense_cache_is_one_page_a_sequence():
+    """Tokens appended one by one to [B, Hkv, S, 128], then attn_fwd over it."""
+    B, Hq, Hkv, S, steps = 3, 8, 2, 256, 3
+    g = torch.Generator().manual_seed(41)
+    cache = [torch.randn((B, Hkv, S, D), generator=g).to(torch.bfloat16) for _ in range(2)]
+    dev = [t.cuda() for t in cache]
+    table = torch.arange(B, dtype=torch.int32).view(B, 1).cuda()
+    for n in range(steps):
+        new = torch.randn((B, Hq + 2 * Hkv, 1, D), generator=g).to(torch.bfloat16)
+        q, k, v = new.split((Hq, Hkv, Hkv), dim=1)
+        at = S - steps + n
+        lens = torch.full((B,), at + 1, dtype=torch.int32)
+        attn.attn_append_paged(k.cuda(), v.cuda(), None, None, dev[0], dev[1], table, lens.cuda())
+        cache[0][:, :, at], cache[1][:, :, at] = k[:, :, 0], v[:, :, 0]
+    for old, now in zip(cache, dev):
+        assert torch.equal(old, now.cpu())
+    o, lse = attn.attn_fwd(q.cuda().contiguous(), dev[0], dev[1])
+    torch.cuda.synchronize()
+    assert compare(o.cpu(), lse.cpu(), *oracle.attention(q, *cache, D ** -0.5, True)).ok()
+
+
 def test_in_place_queries_and_another_stream():
     B, Hq, Hkv, Sq, page, per = 2, 8, 2, 50, 64, 2
     qkv, w, pages, coef, table, cos, sin, _ = make(B, Hq, Hkv, Sq, page, per, 12, True, 128, False, 128)
