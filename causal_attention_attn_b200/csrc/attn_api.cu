@@ -739,7 +739,7 @@ namespace {
 
 // attn_decode_prefix's workspace, cut up.
 struct PrefixSpace {
-    size_t split, pieces, o_suffix, lse_suffix, part_o, part_lse, bytes;  // byte offsets
+    size_t pieces, o_suffix, lse_suffix, part_o, part_lse, bytes;  // byte offsets
 };
 
 // Sized for the whole grid on either part: the lengths, which divide it, are known on the device only.
@@ -754,7 +754,6 @@ PrefixSpace prefix_space(int B, int Hq, const PrefixPlan &pl, const SuffixPlan &
     };
     PrefixSpace sp;
     const size_t rows = static_cast<size_t>(B) * Hq;
-    sp.split = take(sizeof(PrefixSplit));
     sp.pieces = take(sizeof(float) * 2 * pl.grid * kSuffixWarps * suffix_piece(suffix.heads_per_pair));
     sp.o_suffix = take(rows * 128 * sizeof(float));
     sp.lse_suffix = take(rows * sizeof(float));
@@ -829,7 +828,7 @@ extern "C" int attn_decode_prefix(const void *q, const void *k_pages, const void
     DeviceState *s = device_state(&err);
     if (!s)
         return err;
-    const PrefixPlan pl = prefix_plan(B, Hq, Hkv, s->sm_count);
+    PrefixPlan pl = prefix_plan(B, Hq, Hkv, s->sm_count);
     const SuffixPlan suffix = suffix_plan(Hq, Hkv);
     const PrefixSpace sp = prefix_space(B, Hq, pl, suffix);
     if (workspace_bytes < static_cast<long long>(sp.bytes))
@@ -863,8 +862,13 @@ extern "C" int attn_decode_prefix(const void *q, const void *k_pages, const void
     pa.scale = scale;
     pa.plan = pl;
     const long long own_work = own_cap > 0 ? own_pairs * ((own_cap + kSuffixUnitKeys - 1) / kSuffixUnitKeys + kSuffixPairUnits) : 0;
-    const double us = prefix_split(pl, (prefix_cap + 127) / 128, own_work, &pa.fixed);
-    pa.split = us > kFixedSplitUs ? reinterpret_cast<PrefixSplit *>(at(sp.split)) : nullptr;
+    pa.find = choose_split(pl, (prefix_cap + 127) / 128, own_work, &pa.fixed) > kFixedSplitUs;
+    if (!pa.find) {
+        // No more blocks than there can be workers.
+        const long long want = (own_work + kSuffixMinUnits - 1) / kSuffixMinUnits, rest = pl.grid - pa.fixed.ctas;
+        pl.grid = std::max(1, pa.fixed.ctas + static_cast<int>(std::min(want, rest)));
+        pa.plan = pl;
+    }
     pa.part_o = reinterpret_cast<float *>(at(sp.part_o));
     pa.part_lse = reinterpret_cast<float *>(at(sp.part_lse));
     pa.status = s->prefix_status;
@@ -897,8 +901,8 @@ extern "C" int attn_decode_prefix(const void *q, const void *k_pages, const void
     }
     PrefixMergeArgs m;
     m.plan = pl;
+    m.find = pa.find;
     m.fixed = pa.fixed;
-    m.split = pa.split;
     m.B = B;
     m.Hq = Hq;
     m.Hkv = Hkv;

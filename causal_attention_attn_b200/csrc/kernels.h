@@ -163,6 +163,12 @@ struct PrefillFp8Args {
 };
 cudaError_t launch_prefill_fp8(const PrefillFp8Args &a, cudaStream_t stream, int *encode_error);
 
+// The suffixes' part of a decode over a shared prefix: query heads of a pair (see suffix_sm100.cuh), and pairs of a kv head.
+struct SuffixPlan {
+    int heads_per_pair, head_groups;
+};
+SuffixPlan suffix_plan(int Hq, int Hkv);
+
 // The shared-prefix part of a decode over paged caches (head dim 128): B sequences, one new token each,
 // over the prefix's keys. The packed rows of one kv head make tiles of 128, two tiles share a list of KV
 // tiles, and the lists are cut over blocks of the grid (prefix_split.cuh); every (list, block) segment
@@ -176,29 +182,31 @@ struct PrefixPlan {
     int odd;                // a head's last pair has one tile only
     long long lists;
     int grid;               // blocks for prefix and suffixes together
-    float suffix_unit_us;   // an SM's time for one unit of the suffixes
-    FastDiv by_heads;
-    FastDiv by_share;       // a head's blocks (odd: ten times) to those of one full list
+    // The splits to choose from (prefix_split.cuh): the first by_head of 32 give every head equally many
+    // blocks, from tile_pairs to steps more.
+    int by_head, steps;
+    float suffix_unit_us;
+    FastDiv by_steps, by_share, by_rest;
 };
+PrefixPlan prefix_plan(int B, int Hq, int Hkv, int sm_count);
+
 // How one call divides the grid.
 struct PrefixSplit {
     int ctas;                // blocks of the prefix
     int per_list, per_last;  // of each list, and of a head's last list; per_last 0: cut end to end
     __host__ __device__ int per_head(int tile_pairs) const { return (tile_pairs - 1) * per_list + per_last; }
 };
-PrefixPlan prefix_plan(int B, int Hq, int Hkv, int sm_count);
-// The split for a prefix of `tiles` KV tiles and suffixes of `work` units in all, the
-// pairs' own included; what it takes in us.
-double prefix_split(const PrefixPlan &plan, long long tiles, long long work, PrefixSplit *split);
-constexpr double kFixedSplitUs = 24.0;  // see prefix_split.cuh
+// The choice for a prefix of `tiles` KV tiles and suffixes of `work` units, the pairs' own included; its time.
+double choose_split(const PrefixPlan &plan, long long tiles, long long work, PrefixSplit *split);
+constexpr double kFixedSplitUs = 16.0;  // see prefix_split.cuh
 struct PrefixArgs {
     const void *q, *k_pages, *v_pages;
     const int *prefix_table, *prefix_len;  // [prefix_pages], [1]
     int B, Hq, Hkv, num_pages, page_size, prefix_pages, cap;  // cap: most keys of the prefix
     float scale;
     PrefixPlan plan;
+    bool find;  // the split is chosen on the device; otherwise `fixed`
     PrefixSplit fixed;
-    PrefixSplit *split;  // null: `fixed`; otherwise worked out on the device and left here
     float *part_o, *part_lse;
     int *status;
 };
@@ -223,10 +231,6 @@ __host__ __device__ inline int suffix_workers(int total, int ctas)
 }
 // Floats of one piece; a multiple of four, so that every O row can be read 16 bytes at a time.
 __host__ __device__ inline int suffix_piece(int heads_per_pair) { return heads_per_pair * 128 + (heads_per_pair + 3) / 4 * 4; }
-struct SuffixPlan {
-    int heads_per_pair, head_groups;
-};
-SuffixPlan suffix_plan(int Hq, int Hkv);
 struct SuffixArgs {
     const void *q, *k_pages, *v_pages;
     const int *seq_lens, *block_table;
@@ -242,8 +246,8 @@ cudaError_t launch_prefix_decode(const PrefixArgs &a, const SuffixArgs *own, cud
 // Joins the prefix's segments and the suffixes' results into o (bf16) and lse (natural log).
 struct PrefixMergeArgs {
     PrefixPlan plan;
+    bool find;  // as PrefixArgs
     PrefixSplit fixed;
-    const PrefixSplit *split;  // as PrefixArgs
     int B, Hq, Hkv, cap;
     const int *prefix_len;
     const float *part_o, *part_lse;

@@ -106,11 +106,12 @@ namespace {
 // kSplit warps take one row, each every kSplit-th part: lane i looks up where its i-th part lies and
 // its LSE (before any O is read), then each lane adds its four channels over the warp's parts, eight reads
 // in flight, and the warps' sums are joined in shared memory. Bound by the latency of that chain for few
-// rows (four warps a row: see the launch), by reading the parts, still in L2, for many. Where the parts lie follows from the lengths and the split. A row with no part (no prefix, no suffix) gives O = 0 and lse = -inf.
+// rows (four warps a row: see the launch), by reading the parts, still in L2, for many. Where the parts lie follows from the lengths alone and is computed
+// before the wait for the kernel that writes them. A row with no part (no prefix, no suffix) gives O = 0 and lse = -inf.
 constexpr int kMergeWarps = 4;
 constexpr int kMergeSplitRows = 1024;
 
-template <int kSplit>
+template <int kSplit, bool kFind>
 __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const PrefixMergeArgs a)
 {
     constexpr int kTile = 128, D = 128;
@@ -136,12 +137,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const Pr
     }
     const int total = all * pairs;
     PrefixSplit split = a.fixed;
-    if (a.split) {
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        split.ctas = __ldcg(&a.split->ctas);
-        split.per_list = __ldcg(&a.split->per_list);
-        split.per_last = __ldcg(&a.split->per_last);
-    }
+    if constexpr (kFind)
+        split = split_prefix(a.plan, tiles, total, lane);
     // Prefix: the blocks from the one that holds the list's first KV tile to the one that holds its last.
     const int tile = a.by_tile_seqs.quot(b), part_of_heads = a.by_tile_group.quot(h);
     const int in_tile = (b - tile * a.plan.tile_seqs) * a.plan.group + h - part_of_heads * a.plan.group;
@@ -288,9 +285,12 @@ cudaError_t launch_prefix_merge(const PrefixMergeArgs &args, cudaStream_t stream
     static_assert(32 * kMergeWarps == 128, "one thread a channel");
     const int rows = a.B * a.Hq;
     // Up to a block an SM's worth of rows or so, latency counts; beyond it, the work a row costs.
+    const int split_blocks = rows, blocks = (rows + kMergeWarps - 1) / kMergeWarps;
+    auto launch = [&](auto kernel, int grid) { return launch_behind(kernel, grid, 32 * kMergeWarps, 0, stream, true, a); };
     if (rows <= kMergeSplitRows)
-        return launch_behind(prefix_merge_kernel<kMergeWarps>, rows, 32 * kMergeWarps, 0, stream, true, a);
-    return launch_behind(prefix_merge_kernel<1>, (rows + kMergeWarps - 1) / kMergeWarps, 32 * kMergeWarps, 0, stream, true, a);
+        return a.find ? launch(prefix_merge_kernel<kMergeWarps, true>, split_blocks)
+                       : launch(prefix_merge_kernel<kMergeWarps, false>, split_blocks);
+    return a.find ? launch(prefix_merge_kernel<1, true>, blocks) : launch(prefix_merge_kernel<1, false>, blocks);
 }
 
 }  // namespace attn_b200

@@ -54,6 +54,7 @@
 #include <cudaTypedefs.h>
 
 #include <climits>
+#include <algorithm>
 #include <cmath>
 #include <mutex>
 
@@ -146,7 +147,7 @@ struct Params {
     // head's group) packed into tiles of prefix.tile_seqs sequences. block_table is the prefix's one row,
     // seq_lens its one length; O and LSE leave as fp32 partials, 256 rows for each segment.
     PrefixPlan prefix{};
-    PrefixSplit fixed{}, *split = nullptr;  // as PrefixArgs
+    PrefixSplit fixed{};
     float *part_o = nullptr;    // [segment slot][256][128]
     float *part_lse = nullptr;  // [segment slot][256], log2 units
 };
@@ -281,14 +282,14 @@ struct Segments {
     int begin, end;       // this CTA's range
     int first_list;       // list that holds `begin`
 };
-__shared__ PrefixSplit s_split;  // when it is worked out here
+__shared__ PrefixSplit s_split;
 __shared__ Segments s_segments;
 
-__device__ __forceinline__ Segments find_segments(const Params &p, const PrefixSplit &split, int len)
+__device__ __forceinline__ Segments find_segments(const Params &p, const PrefixSplit &split)
 {
     Segments sg;
-    sg.len = len;
-    sg.tiles = (len + kBN - 1) / kBN;
+    sg.len = prefix_length(p);
+    sg.tiles = (sg.len + kBN - 1) / kBN;
     const int cta = static_cast<int>(blockIdx.x), pairs = p.prefix.tile_pairs;
     if (split.per_last > 0) {
         const int per_head = split.per_head(pairs), head = cta / per_head;
@@ -404,7 +405,7 @@ __device__ __forceinline__ int next_active(const Params &p, int r)
     }
 }
 
-template <int D, int kMode>
+template <int D, int kMode, bool kFind = false>  // kFind (shared prefix): s_split holds the split
 __device__ __forceinline__ void run_tiles(const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                                           const CUtensorMap &tm_o, const Params &p, uint8_t *smem_raw)
 {
@@ -470,7 +471,7 @@ __device__ __forceinline__ void run_tiles(const CUtensorMap &tm_q, const CUtenso
         }
         fence_proxy_async_smem();
         if (warp == 11 && lane == 0)
-            s_segments = find_segments(p, p.split ? s_split : p.fixed, prefix_length(p));
+            s_segments = find_segments(p, kFind ? s_split : p.fixed);
     }
     if (warp == kWarpTma && lane == 0) {
         tma_prefetch_desc(&tm_q);
@@ -1097,10 +1098,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     run_tiles<D, kMode>(tm_q, tm_k, tm_v, tm_o, p, smem_raw);
 }
 
-// Decode over a shared prefix: the grid's first blocks take the prefix, the rest the suffixes, as
-// split_prefix divides them. One launch, because neither needs the other, and the merge behind it then
-// waits for one grid. (No suffixes: sp.seq_lens is null.)
-template <int kGroups>
+// Decode over a shared prefix: the grid's first blocks take the prefix, the rest the suffixes, as the split
+// says, which is fixed or (kFind) worked out from the lengths. One launch, because neither needs the other,
+// and the merge behind it then waits for one grid. (No suffixes: sp.seq_lens is null.)
+template <int kGroups, bool kFind>
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_sk,
@@ -1111,7 +1112,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("griddepcontrol.launch_dependents;");  // the merge, which waits for this grid's end
     const int cta = static_cast<int>(blockIdx.x);
     int ctas = p.fixed.ctas;
-    if (p.split) {
+    if constexpr (kFind) {
+        // (Beside the prefix's set-up, in every block, this took a us longer.)
         if (threadIdx.x < 32) {
             const int lane = static_cast<int>(threadIdx.x), tiles = (prefix_length(p) + kBN - 1) / kBN;
             int work = 0;
@@ -1121,17 +1123,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 work = __reduce_add_sync(0xffffffffu, work) * sp.Hkv * sp.head_groups;
             }
             const PrefixSplit split = split_prefix(p.prefix, tiles, work, lane);
-            if (lane == 0) {
+            if (lane == 0)
                 s_split = split;
-                if (cta == 0)
-                    *p.split = split;
-            }
         }
         __syncthreads();
         ctas = s_split.ctas;
     }
     if (cta < ctas)
-        run_tiles<128, kPrefix>(tm_q, tm_k, tm_v, tm_q, p, smem_raw);
+        run_tiles<128, kPrefix, kFind>(tm_q, tm_k, tm_v, tm_q, p, smem_raw);
     else if (sp.seq_lens)
         suffix::run<kGroups>(tm_sk, tm_sv, sp, smem_raw, cta - ctas, static_cast<int>(gridDim.x) - ctas);
 }
@@ -1276,21 +1275,24 @@ PrefixPlan prefix_plan(int B, int Hq, int Hkv, int sm_count)
     pl.tile_pairs = (tiles + 1) / 2;
     pl.odd = tiles % 2;
     pl.lists = static_cast<long long>(pl.heads) * pl.tile_pairs;
-    pl.grid = sm_count > 2 ? sm_count : 2;  // one block for each part at least
-    pl.suffix_unit_us = Hq / Hkv > 8 ? 0.098f : 0.074f;
-    pl.by_heads = FastDiv(pl.heads);
+    pl.grid = std::max(sm_count, 2);  // one block for each part at least
+    const int counts = pl.grid / pl.heads - pl.tile_pairs + 1;
+    pl.by_head = std::min(std::max(counts, 0), 24);
+    pl.steps = counts - 1;
+    pl.by_steps = FastDiv(std::max(pl.by_head - 1, 1));
     pl.by_share = FastDiv(pl.odd ? 10 * (pl.tile_pairs - 1) + 8 : pl.tile_pairs);
+    pl.by_rest = FastDiv(32 - pl.by_head);
+    pl.suffix_unit_us = Hq / Hkv > 8 ? 0.098f : 0.074f;
     return pl;
 }
 
-double prefix_split(const PrefixPlan &plan, long long tiles, long long work, PrefixSplit *split)
+double choose_split(const PrefixPlan &plan, long long tiles, long long work, PrefixSplit *split)
 {
-    *split = PrefixSplit{};
+    *split = PrefixSplit{0, 0, 0};
     if (tiles == 0)
         return 0.0;
     float best = INFINITY;
-    const int n = split_candidates(plan);
-    for (int i = 0; i < n; ++i) {
+    for (int i = 0; i < 32; ++i) {
         PrefixSplit s;
         const float us = split_candidate(plan, i, static_cast<float>(tiles), static_cast<float>(work), &s);
         if (us < best) {
@@ -1358,7 +1360,6 @@ cudaError_t launch_prefix_decode(const PrefixArgs &a, const SuffixArgs *own, cud
     p.group = pl.group;
     p.prefix = pl;
     p.fixed = a.fixed;
-    p.split = a.split;
     p.scale_log2 = a.scale * kLog2e;
     p.seq_lens = a.prefix_len;
     p.block_table = a.prefix_table;
@@ -1369,7 +1370,7 @@ cudaError_t launch_prefix_decode(const PrefixArgs &a, const SuffixArgs *own, cud
     p.part_o = a.part_o;
     p.part_lse = a.part_lse;
     constexpr int kSmem = C::kSmem > suffix::kSmem ? C::kSmem : suffix::kSmem;
-    static bool set[2][kMaxDevices] = {};
+    static bool set[4][kMaxDevices] = {};
     auto launch = [&](auto kernel, bool (&done)[kMaxDevices]) {
         const cudaError_t ready = prepare(kernel, kSmem, done);
         if (ready != cudaSuccess)
@@ -1377,7 +1378,9 @@ cudaError_t launch_prefix_decode(const PrefixArgs &a, const SuffixArgs *own, cud
         kernel<<<static_cast<unsigned>(pl.grid), kThreads, kSmem, stream>>>(tq, tk, tv, tsk, tsv, p, sp);
         return cudaGetLastError();
     };
-    return own && own->plan.heads_per_pair > 8 ? launch(prefix_decode_kernel<2>, set[1]) : launch(prefix_decode_kernel<1>, set[0]);
+    if (own && own->plan.heads_per_pair > 8)
+        return a.find ? launch(prefix_decode_kernel<2, true>, set[3]) : launch(prefix_decode_kernel<2, false>, set[2]);
+    return a.find ? launch(prefix_decode_kernel<1, true>, set[1]) : launch(prefix_decode_kernel<1, false>, set[0]);
 }
 
 }  // namespace attn_b200

@@ -4,7 +4,7 @@
  *
  * The first `ctas` blocks of the grid take the prefix, the rest the suffixes, side by side: the prefix is
  * bound by its softmax and tensor work, the suffixes by memory, and neither waits for the other (one behind
- * the other, 125 sequences of up to 768 keys behind 32,749 took 79 us instead of 65). A model of both
+ * the other, 125 sequences of up to 768 keys behind 32,749 took 79 us instead of 63). A model of both
  * times, measured, says which split ends first, a tenth of the prefix's added so that of splits that end
  * alike it takes the one with the shorter prefix:
  *   prefix     4 us, and for each KV tile of a block 1.6 us, or 1.4 us in a list of one query tile;
@@ -15,11 +15,14 @@
  * then gets fewer), so that a block has one segment; or, where that fits badly, all lists laid end to end
  * are cut evenly and most blocks have two, 3 us more.
  *
- * The lengths are known on the device only. There the blocks work the split out, each for itself and all
- * alike, and one leaves it for the merge, which costs 3 us. So for calls that take no more than
- * kFixedSplitUs by their greatest lengths the host fixes the split from those. 32 sequences of up to 512
- * keys behind 4,096 take 20.0 us so and 23.2 by the device's split; when they hold a fifth of that, 19.4 and
- * 18.3. For 128 sequences, a longer call, the last two are 39.7 and 27.3.
+ * Of the splits that there can be, 32 are compared. The lengths are known on the device only: there a warp of
+ * each block compares them, one a lane, and the merge does the same before it waits for the blocks, every
+ * operation with its rounding named, so that all come to one choice. (32 prepared splits read from the
+ * kernel's parameters took 2 to 4 us longer, the choice left in memory for the merge 1.5 us.) That takes 1 to
+ * 1.5 us, so for short calls (kFixedSplitUs by the model) the host fixes the split, from the greatest lengths
+ * that the call allows: 32 sequences of up to 512 keys behind 4,096, the first to be left to the device,
+ * take 21.9 us with it and 20.7 with a fixed split, 18.7 and 19.4 when half as long; 128 of
+ * them 55 either way, 36 and 41.
  */
 #pragma once
 
@@ -31,16 +34,37 @@
 
 namespace attn_b200 {
 
-__host__ __device__ __forceinline__ float about_quotient(float a, float b)
+__host__ __device__ __forceinline__ float times(float a, float b)
 {
 #ifdef __CUDA_ARCH__
-    return __fdividef(a, b);
+    return __fmul_rn(a, b);
 #else
-    return a / b;
+    return a * b;
 #endif
 }
 
-__host__ __device__ __forceinline__ float about_root(float x)
+__host__ __device__ __forceinline__ float plus(float a, float b)
+{
+#ifdef __CUDA_ARCH__
+    return __fadd_rn(a, b);
+#else
+    return a + b;
+#endif
+}
+
+// 1 / n and the square root, to a few units in the last place.
+__host__ __device__ __forceinline__ float one_over(int n)
+{
+#ifdef __CUDA_ARCH__
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(__int2float_rn(n)));
+    return y;
+#else
+    return 1.0f / static_cast<float>(n);
+#endif
+}
+
+__host__ __device__ __forceinline__ float root(float x)
 {
 #ifdef __CUDA_ARCH__
     float y;
@@ -51,60 +75,47 @@ __host__ __device__ __forceinline__ float about_root(float x)
 #endif
 }
 
-// Candidate i of all splits, and its model time in us; infinity when there is none. Any split is right,
-// so the times are rounded as it comes.
+// Split i of 32, and what it takes (us).
 __host__ __device__ __forceinline__ float split_candidate(const PrefixPlan &p, int i, float tiles, float work, PrefixSplit *s)
 {
-    auto up = [](float n, int parts) { return ceilf(about_quotient(n, static_cast<float>(parts)) - 1e-3f); };
-    const int most = p.grid - (work > 0.f ? 1 : 0);
+    auto up = [](float n) { return ceilf(plus(n, -1e-3f)); };
+    const int pairs = p.tile_pairs;
     float us;
-    if (i < 32) {  // end to end
-        s->ctas = most * (i + 1) / 32 > 1 ? most * (i + 1) / 32 : 1;
-        s->per_list = s->per_last = 0;
-        us = 4.0f + 3.0f * up(static_cast<float>(p.lists), s->ctas) + 1.6f * up(tiles * static_cast<float>(p.lists), s->ctas);
-    } else {  // a head's blocks: a share for each full list, the rest for the last (a single tile's: 0.8 of one)
-        const int each = p.tile_pairs + i - 32;
+    if (i < p.by_head) {  // a head's blocks: a share for each full list, the rest for the last (a single tile's: 0.8 of one)
+        const int each = pairs + static_cast<int>(p.by_steps.quot(static_cast<unsigned>(p.steps * i)));
+        const int share = static_cast<int>(p.by_share.quot(static_cast<unsigned>(p.odd ? 10 * each : each)));
+        s->per_list = pairs == 1 ? 0 : share > 1 ? share : 1;
+        s->per_last = each - (pairs - 1) * s->per_list;
         s->ctas = each * p.heads;
-        if (s->ctas > most)
-            return INFINITY;
-        const int share = static_cast<int>(p.by_share.quot(p.odd ? 10 * each : each));
-        s->per_list = p.tile_pairs == 1 ? 0 : share > 1 ? share : 1;
-        s->per_last = each - (p.tile_pairs - 1) * s->per_list;
-        us = 4.0f + fmaxf(s->per_list ? 1.6f * up(tiles, s->per_list) : 0.f, (p.odd ? 1.4f : 1.6f) * up(tiles, s->per_last));
+        const float full = s->per_list ? times(1.6f, up(times(tiles, one_over(s->per_list)))) : 0.f;
+        us = plus(4.0f, fmaxf(full, times(p.odd ? 1.4f : 1.6f, up(times(tiles, one_over(s->per_last))))));
+    } else {  // end to end
+        const int ctas = static_cast<int>(p.by_rest.quot(static_cast<unsigned>(p.grid * (32 - i))));
+        s->ctas = ctas > 1 ? ctas : 1;
+        s->per_list = s->per_last = 0;
+        const float lists = times(static_cast<float>(p.lists), one_over(s->ctas));
+        us = plus(plus(4.0f, times(3.0f, up(lists))), times(1.6f, up(times(tiles, lists))));
     }
-    const float own_us = about_quotient(p.suffix_unit_us, static_cast<float>(p.grid - s->ctas));
-    return 0.1f * us + (work > 0.f ? fmaxf(us, 4.0f + work * about_root(own_us * own_us + 0.0007f * 0.0007f)) : us);
+    float ends = us;
+    if (work > 0.f) {
+        const float own = times(p.suffix_unit_us, one_over(p.grid - s->ctas));  // infinite without a block for it
+        ends = fmaxf(us, plus(4.0f, times(work, root(plus(times(own, own), 0.0007f * 0.0007f)))));
+    }
+    return plus(times(0.1f, us), ends);
 }
 
-// The number of candidates, from the most blocks that one head can have.
-__host__ __device__ __forceinline__ int split_candidates(const PrefixPlan &p)
-{
-    const int each = p.by_heads.quot(p.grid) - p.tile_pairs + 1;
-    return 32 + (each > 0 ? each : 0);
-}
-
-// By a whole warp; every lane gets the result. `tiles`: KV tiles of the prefix, `work`: all suffixes' units,
+// By a whole warp; every lane gets the choice. `tiles`: KV tiles of the prefix; `work`: all suffixes' units,
 // the pairs' own included.
 __device__ __forceinline__ PrefixSplit split_prefix(const PrefixPlan &p, int tiles, int work, int lane)
 {
-    PrefixSplit mine{}, s;
-    if (tiles == 0)
-        return mine;
-    float best = INFINITY;
-    const int n = split_candidates(p);
-    for (int i = lane; i < n; i += 32) {
-        const float us = split_candidate(p, i, static_cast<float>(tiles), static_cast<float>(work), &s);
-        if (us < best) {
-            best = us;
-            mine = s;
-        }
-    }
-    const unsigned least = __reduce_min_sync(0xffffffffu, __float_as_uint(best));  // times are positive
-    const int from = __ffs(__ballot_sync(0xffffffffu, __float_as_uint(best) == least)) - 1;
-    s.ctas = __shfl_sync(0xffffffffu, mine.ctas, from);
-    s.per_list = __shfl_sync(0xffffffffu, mine.per_list, from);
-    s.per_last = __shfl_sync(0xffffffffu, mine.per_last, from);
-    return s;
+    PrefixSplit s;
+    const unsigned us = __float_as_uint(split_candidate(p, lane, __int2float_rn(tiles), __int2float_rn(work), &s));  // positive
+    const unsigned least = __reduce_min_sync(0xffffffffu, us);
+    const int best = __ffs(__ballot_sync(0xffffffffu, us == least)) - 1;
+    s.ctas = __shfl_sync(0xffffffffu, s.ctas, best);
+    s.per_list = __shfl_sync(0xffffffffu, s.per_list, best);
+    s.per_last = __shfl_sync(0xffffffffu, s.per_last, best);
+    return tiles > 0 ? s : PrefixSplit{0, 0, 0};
 }
 
 // Units of 16 keys of one suffix, and with what each pair counts on top.
