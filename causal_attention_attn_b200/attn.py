@@ -664,9 +664,9 @@ def attn_qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor | 
     _, dqs = _rows("dq", dq, dev, qshape)
     _, dks = _rows("dk", dk, dev, kshape)
     dwq = dwk = ws = None
-    if qw is not None:
-        dwq, dwk = q.new_empty((D,), dtype=torch.float32), q.new_empty((D,), dtype=torch.float32)
-        ws = q.new_empty((_NORM_ROPE_BWD_BLOCKS * 2 * D,), dtype=torch.float32)
+    if qw is not None and kw is not None:  # (one alone: the library refuses it)
+        dwq, dwk = torch.empty_like(q_weight, dtype=torch.float32), torch.empty_like(k_weight, dtype=torch.float32)
+        ws = torch.empty(_NORM_ROPE_BWD_BLOCKS * 2 * D, dtype=torch.float32, device=q.device)
         _used_on(stream, dwq, dwk, ws)
     _call(load_library().attn_qk_norm_rope_bwd, dev, stream, q.data_ptr(), k.data_ptr(), qw, kw, _ptr(cos), _ptr(sin), pos,
           dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), _ptr(dwq), _ptr(dwk), _ptr(ws), B, Hq, Hkv, S,

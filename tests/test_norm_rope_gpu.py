@@ -256,3 +256,7 @@ def test_refusals():
     with pytest.raises(attn.AttnError) as e:
         attn.attn_qk_norm_rope(x, x, cos, sin, q_weight=torch.ones(64, dtype=torch.bfloat16, device="cuda"))
     assert e.value.status == -1
+    for one in ("q_weight", "k_weight"):
+        with pytest.raises(attn.AttnError) as e:
+            attn.attn_qk_norm_rope_bwd(x, x, cos, sin, x, x, **{one: torch.ones(64, dtype=torch.bfloat16, device="cuda")})
+        assert e.value.status == -1
