@@ -192,7 +192,8 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendParams 
                         const int e = 4 * j + t;  // of the lane's sixteen
                         v[t] = kInterleaved ? ((e & 1) ? x[k].B[e >> 1] : x[k].A[e >> 1]) : (e < 8 ? x[k].A[e & 7] : x[k].B[e & 7]);
                     }
-                    codes[j] = quotient_codes(v[0], v[1], f.x, f.y) | (quotient_codes(v[2], v[3], f.z, f.w) << 16);  // the first in the low byte
+                    // The first element in the low byte.
+                    codes[j] = quotient_codes(v[0], v[1], f.x, f.y) | (quotient_codes(v[2], v[3], f.z, f.w) << 16);
                 }
                 uint8_t *out = static_cast<uint8_t *>(p.pages[kind - kK]) + dst + (k ? next_head : 0);
                 *reinterpret_cast<uint2 *>(out + le.e0) = make_uint2(codes[0], codes[1]);

@@ -106,8 +106,10 @@ namespace {
 // kSplit warps take one row, each every kSplit-th part: lane i looks up where its i-th part lies and
 // its LSE (before any O is read), then each lane adds its four channels over the warp's parts, eight reads
 // in flight, and the warps' sums are joined in shared memory. Bound by the latency of that chain for few
-// rows (four warps a row: see the launch), by reading the parts, still in L2, for many. Where the parts lie follows from the lengths alone and is computed
-// before the wait for the kernel that writes them. A row with no part (no prefix, no suffix) gives O = 0 and lse = -inf.
+// rows (four warps a row: see the launch), by reading the parts, still in L2, for many. Where the parts lie
+// follows from the lengths alone and is computed before the wait for the kernel that writes them (kFind: the
+// split of that kernel's grid too, from the same lengths). A row with no part (no prefix, no suffix) gives
+// O = 0 and lse = -inf.
 constexpr int kMergeWarps = 4;
 constexpr int kMergeSplitRows = 1024;
 

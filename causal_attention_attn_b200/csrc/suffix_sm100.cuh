@@ -6,9 +6,9 @@
  * What it has to do is read every suffix's K and V once; the suffixes are many, short and of different
  * lengths. So the worker is one warp, not a CTA: a pair is one (sequence, kv head, up to 16 of its query
  * heads), its keys are units of 16, all pairs' units are laid end to end, two more before each pair for
- * what its start and end cost a warp, and cut evenly over the warps of the grid (EvenRange). Each warp streams its units through a ring of its own by TMA and no warp
- * waits for another, so the start and the end of a pair are hidden behind the other eleven warps of the
- * SM. (The CTA-wide paged decode kernel, whose 128-key chunks pass through one softmax, took 53 us where
+ * what its start and end cost a warp, and cut evenly over the warps of the grid (EvenRange). Each warp
+ * streams its units through a ring of its own by TMA and no warp waits for another, so the start and the
+ * end of a pair are hidden behind the other eleven warps of the SM. (The CTA-wide paged decode kernel, whose 128-key chunks pass through one softmax, took 53 us where
  * this takes 31, for 125 sequences of up to 768 keys and 6 kv heads: it drains at every pair.)
  *
  * Per unit, K and V [16 keys][128] in shared memory (128-byte swizzle), heads in groups of eight:
@@ -116,7 +116,8 @@ __device__ __forceinline__ void run(const CUtensorMap &tm_k, const CUtensorMap &
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffMisc);
-    int *start = reinterpret_cast<int *>(smem + kOffStart), *before = reinterpret_cast<int *>(smem + kOffUnits), *len = reinterpret_cast<int *>(smem + kOffLen);
+    int *start = reinterpret_cast<int *>(smem + kOffStart), *before = reinterpret_cast<int *>(smem + kOffUnits);
+    int *len = reinterpret_cast<int *>(smem + kOffLen);
     const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(warp * kStages * kStageBytes);
     const uint32_t bar0 = smem_u32(smem) + kOffBar + static_cast<uint32_t>(warp * kStages * 8);
     const int pairs = p.Hkv * p.head_groups;  // of a sequence
