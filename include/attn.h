@@ -452,11 +452,12 @@ int attn_append_paged(const void *q, const void *k, const void *v, const void *q
 
 /*
  * attn_append_paged_fp8 — attn_append_paged to an e4m3 cache (attn_decode_paged_fp8's): the stored
- * code of a key or value element x of kv head g, channel d is the e4m3 value nearest to
+ * code of a key or value element x of kv head g, channel d is the e4m3 value nearest to the fp32 quotient
  * x / k_scale[g, d] (v_scale), ties to even, magnitudes above 448 stored as 448, NaN as NaN; x is the
- * fp32 value, not rounded to bf16 first, and the quotient is computed in fp32 to within 2 units in
- * the last place. k_scale, v_scale: fp32 [Hkv, 128], the cache's coefficients, each in
- * [2^-126, 2^126].
+ * fp32 value, not rounded to bf16 first. For elements stored as they came (values, and keys without norm
+ * and rotation) that is the correctly rounded quotient's code; for a computed key's the quotient is within
+ * a unit in the last place, and exact on a tie. k_scale, v_scale: fp32 [Hkv, 128], the cache's
+ * coefficients, each in [2^-93, 2^126] (from 2^-126 on with the quotient within 3 units).
  * Every other argument and rule is attn_append_paged's.
  */
 int attn_append_paged_fp8(const void *q, const void *k, const void *v, const void *q_weight, const void *k_weight,
