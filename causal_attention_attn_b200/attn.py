@@ -4,6 +4,10 @@ Argument marshalling only: tensors are checked for dtype/device/contiguity, thei
 the current CUDA stream are passed to the C entry points, and a non-zero status becomes an
 ``AttnError``. PyTorch supplies device memory and streams; every step of the attention itself runs
 in the library's kernels. There is no fallback: if the library is missing the call fails.
+
+``stream`` (a torch stream or a handle; default the current stream) is where a call runs. Its inputs
+have to be ready there and to stay until it is done; what the call allocates itself, results and
+workspaces, is that stream's memory and may be dropped at any time.
 """
 from __future__ import annotations
 
@@ -117,6 +121,32 @@ def _stream_handle(stream) -> int:
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _side(stream, dev: int):
+    """The stream that a call on `stream` allocates for, or None when that is the current one."""
+    if stream is None:
+        return None
+    handle = _stream_handle(stream)
+    if handle == torch._C._cuda_getCurrentRawStream(dev):
+        return None
+    if handle in (0, 1):  # both name the legacy default stream
+        return torch.cuda.default_stream(dev)
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle, device=dev)
+
+
+def _new(side, make, *args, **kw):
+    """Memory that this module allocates for a call: make(...). The caching allocator orders a block's
+    next use behind the stream that it was allocated on, so with a `side` stream it is that stream's block:
+    what had it before is behind the call, and what gets it when it is dropped, behind the call too. The
+    current stream, where a result is usually read next, is recorded beside it."""
+    if side is None:
+        return make(*args, **kw)
+    current = torch.cuda.current_stream(side.device)
+    with torch.cuda.stream(side):
+        t = make(*args, **kw)
+    t.record_stream(current)
+    return t
+
+
 def _check_tensor(name, t, dtype, ndim):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -183,14 +213,15 @@ def attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: float | N
         raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}")
     if scale is None:
         scale = D ** -0.5
+    side = _side(stream, q.get_device())
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        out = _new(side, torch.empty, q.shape, dtype=torch.bfloat16, device=q.device)
     else:
         _check_rows("out", out, torch.bfloat16)
         if out.shape != q.shape:
             raise ValueError("out must have the shape of q")
     if lse is None:
-        lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device)
+        lse = _new(side, torch.empty, (B, Hq, Sq), dtype=torch.float32, device=q.device)
     else:
         _check_tensor("lse", lse, torch.float32, 3)
         if tuple(lse.shape) != (B, Hq, Sq):
@@ -233,11 +264,11 @@ def attn_fwd_host(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: floa
         scale = D ** -0.5
     stream = stream or torch.cuda.current_stream(device)
     if dev_bufs is None:
-        dev_bufs = (torch.empty(q.shape, dtype=torch.bfloat16, device=device),
-                    torch.empty(k.shape, dtype=torch.bfloat16, device=device),
-                    torch.empty(v.shape, dtype=torch.bfloat16, device=device),
-                    torch.empty(q.shape, dtype=torch.bfloat16, device=device),
-                    torch.empty((B, Hq, Sq), dtype=torch.float32, device=device))
+        dev = torch.device(device).index
+        side = _side(stream, torch.cuda.current_device() if dev is None else dev)
+        dev_bufs = [_new(side, torch.empty, shape, dtype=torch.bfloat16, device=device)
+                    for shape in (q.shape, k.shape, v.shape, q.shape)]
+        dev_bufs.append(_new(side, torch.empty, (B, Hq, Sq), dtype=torch.float32, device=device))
     qd, kd, vd, od, ld = dev_bufs
     if out_host is None:
         out_host = torch.empty(q.shape, dtype=torch.bfloat16, pin_memory=True)
@@ -270,8 +301,9 @@ def attn_decode_noalloc(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale
         raise ValueError(f"expected q [B,Hq,1,D] and k, v [B,Hkv,Skv,D]; got {tuple(q.shape)}, {tuple(k.shape)}")
     if scale is None:
         scale = D ** -0.5
-    out = torch.empty_like(q) if out is None else out
-    lse = torch.empty((B, Hq, 1), dtype=torch.float32, device=q.device) if lse is None else lse
+    side = _side(stream, q.get_device())
+    out = _new(side, torch.empty_like, q) if out is None else out
+    lse = _new(side, torch.empty, (B, Hq, 1), dtype=torch.float32, device=q.device) if lse is None else lse
     _check_tensor("out", out, torch.bfloat16, 4)
     _check_tensor("lse", lse, torch.float32, 3)
     with torch.cuda.device(q.device):
@@ -304,8 +336,9 @@ def attn_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Ten
         raise ValueError("block_table and seq_lens need one row / entry per batch element")
     if scale is None:
         scale = D ** -0.5
-    out = torch.empty_like(q) if out is None else out
-    lse = torch.empty((B, Hq, 1), dtype=torch.float32, device=q.device) if lse is None else lse
+    side = _side(stream, q.get_device())
+    out = _new(side, torch.empty_like, q) if out is None else out
+    lse = _new(side, torch.empty, (B, Hq, 1), dtype=torch.float32, device=q.device) if lse is None else lse
     _check_tensor("out", out, torch.bfloat16, 4)
     _check_tensor("lse", lse, torch.float32, 3)
     with torch.cuda.device(q.device):
@@ -340,8 +373,9 @@ def attn_prefill_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Te
         raise ValueError("block_table and seq_lens need one row / entry per batch element")
     if scale is None:
         scale = D ** -0.5
-    out = torch.empty_like(q) if out is None else out
-    lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device) if lse is None else lse
+    side = _side(stream, q.get_device())
+    out = _new(side, torch.empty_like, q) if out is None else out
+    lse = _new(side, torch.empty, (B, Hq, Sq), dtype=torch.float32, device=q.device) if lse is None else lse
     _check_tensor("out", out, torch.bfloat16, 4)
     _check_tensor("lse", lse, torch.float32, 3)
     with torch.cuda.device(q.device):
@@ -379,8 +413,9 @@ def attn_decode_fp8(q: torch.Tensor, k8: torch.Tensor, v8: torch.Tensor, k_scale
         raise ValueError("expected q [B,Hq,1,D], k8, v8 [B,Hkv,Skv,D] and scales [Hkv,D]")
     if scale is None:
         scale = D ** -0.5
-    out = torch.empty_like(q) if out is None else out
-    lse = torch.empty((B, Hq, 1), dtype=torch.float32, device=q.device) if lse is None else lse
+    side = _side(stream, q.get_device())
+    out = _new(side, torch.empty_like, q) if out is None else out
+    lse = _new(side, torch.empty, (B, Hq, 1), dtype=torch.float32, device=q.device) if lse is None else lse
     _check_tensor("out", out, torch.bfloat16, 4)
     _check_tensor("lse", lse, torch.float32, 3)
     with torch.cuda.device(q.device):
@@ -408,8 +443,9 @@ def attn_prefill_fp8(q: torch.Tensor, k8: torch.Tensor, v8: torch.Tensor, k_scal
         raise ValueError("expected q [B,Hq,Sq,D], k8, v8 [B,Hkv,Skv,D] and scales [Hkv,D]")
     if scale is None:
         scale = D ** -0.5
-    out = torch.empty_like(q) if out is None else out
-    lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device) if lse is None else lse
+    side = _side(stream, q.get_device())
+    out = _new(side, torch.empty_like, q) if out is None else out
+    lse = _new(side, torch.empty, (B, Hq, Sq), dtype=torch.float32, device=q.device) if lse is None else lse
     _check_tensor("out", out, torch.bfloat16, 4)
     _check_tensor("lse", lse, torch.float32, 3)
     with torch.cuda.device(q.device):
@@ -441,8 +477,9 @@ def attn_decode_paged_fp8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch
         raise ValueError("block_table and seq_lens need one row / entry per batch element")
     if scale is None:
         scale = D ** -0.5
-    out = torch.empty_like(q) if out is None else out
-    lse = torch.empty((B, Hq, 1), dtype=torch.float32, device=q.device) if lse is None else lse
+    side = _side(stream, q.get_device())
+    out = _new(side, torch.empty_like, q) if out is None else out
+    lse = _new(side, torch.empty, (B, Hq, 1), dtype=torch.float32, device=q.device) if lse is None else lse
     _check_tensor("out", out, torch.bfloat16, 4)
     _check_tensor("lse", lse, torch.float32, 3)
     with torch.cuda.device(q.device):
@@ -495,9 +532,10 @@ def attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
         raise ValueError("shapes of q, k, v, o, lse, dout disagree")
     if scale is None:
         scale = D ** -0.5
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    side = _side(stream, q.get_device())
+    dq = _new(side, torch.empty_like, q) if dq is None else dq
+    dk = _new(side, torch.empty_like, k) if dk is None else dk
+    dv = _new(side, torch.empty_like, v) if dv is None else dv
     with torch.cuda.device(q.device):
         rc = load_library().attn_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dout.data_ptr(),
                                      lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Hq, Hkv, Sq, Skv, D,
@@ -596,17 +634,8 @@ def _positions(positions, B, S, dev):
     return positions.data_ptr()
 
 
-def _new_rows(like):
-    return torch.empty_like(like, memory_format=torch.contiguous_format)
-
-
-def _used_on(stream, *tensors):
-    """Memory that this module allocated and a stream other than the current one uses: the caching
-    allocator may hand it out again only behind that stream."""
-    if stream is not None:
-        used = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
-        for t in tensors:
-            t.record_stream(used)
+def _new_rows(like, side):
+    return _new(side, torch.empty_like, like, memory_format=torch.contiguous_format)
 
 
 def attn_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor | None, sin: torch.Tensor | None,
@@ -630,8 +659,9 @@ def attn_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor | None
         raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}")
     rot_dim, max_pos = _rotation(cos, sin, D, dev)
     qw, kw, pos = _weight("q_weight", q_weight, D, dev), _weight("k_weight", k_weight, D, dev), _positions(positions, B, S, dev)
-    q_out = _new_rows(q) if q_out is None else q_out
-    k_out = _new_rows(k) if k_out is None else k_out
+    side = _side(stream, dev)
+    q_out = _new_rows(q, side) if q_out is None else q_out
+    k_out = _new_rows(k, side) if k_out is None else k_out
     _, qos = _rows("q_out", q_out, dev, qshape)
     _, kos = _rows("k_out", k_out, dev, kshape)
     _call(load_library().attn_qk_norm_rope, dev, stream, q.data_ptr(), k.data_ptr(), qw, kw, _ptr(cos), _ptr(sin), pos,
@@ -659,15 +689,15 @@ def attn_qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor | 
     _, dkos = _rows("dk_out", dk_out, dev, kshape)
     rot_dim, max_pos = _rotation(cos, sin, D, dev)
     qw, kw, pos = _weight("q_weight", q_weight, D, dev), _weight("k_weight", k_weight, D, dev), _positions(positions, B, S, dev)
-    dq = _new_rows(q) if dq is None else dq
-    dk = _new_rows(k) if dk is None else dk
+    side = _side(stream, dev)
+    dq = _new_rows(q, side) if dq is None else dq
+    dk = _new_rows(k, side) if dk is None else dk
     _, dqs = _rows("dq", dq, dev, qshape)
     _, dks = _rows("dk", dk, dev, kshape)
     dwq = dwk = ws = None
     if qw is not None and kw is not None:  # (one alone: the library refuses it)
-        dwq, dwk = torch.empty_like(q_weight, dtype=torch.float32), torch.empty_like(k_weight, dtype=torch.float32)
-        ws = torch.empty(_NORM_ROPE_BWD_BLOCKS * 2 * D, dtype=torch.float32, device=q.device)
-        _used_on(stream, dwq, dwk, ws)
+        dwq, dwk = (_new(side, torch.empty_like, w, dtype=torch.float32) for w in (q_weight, k_weight))
+        ws = _new(side, torch.empty, _NORM_ROPE_BWD_BLOCKS * 2 * D, dtype=torch.float32, device=q.device)
     _call(load_library().attn_qk_norm_rope_bwd, dev, stream, q.data_ptr(), k.data_ptr(), qw, kw, _ptr(cos), _ptr(sin), pos,
           dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), _ptr(dwq), _ptr(dwk), _ptr(ws), B, Hq, Hkv, S,
           D, qs, ks, dqos, dkos, dqs, dks, rot_dim, max_pos, 1 if interleaved else 0, eps)
@@ -705,7 +735,7 @@ def _append(k, v, cos, sin, k_pages, v_pages, k_scale, v_scale, block_table, seq
         Bq, Hq, S, Dq = qshape
         if Bq != B or S != Sq or Dq != D:
             raise ValueError(f"q must be [{B}, Hq, {Sq}, {D}], got {tuple(q.shape)}")
-        q_out = _new_rows(q) if q_out is None else q_out
+        q_out = _new_rows(q, _side(stream, dev)) if q_out is None else q_out
         _, qos = _rows("q_out", q_out, dev, qshape)
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -790,13 +820,13 @@ def attn_decode_prefix(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Te
         raise ValueError("block_table and seq_lens need one row / entry per batch element, prefix_len one entry")
     if scale is None:
         scale = D ** -0.5
-    out = torch.empty_like(q) if out is None else out
-    lse = q.new_empty((B, Hq, 1), dtype=torch.float32) if lse is None else lse
+    side = _side(stream, dev)
+    out = _new(side, torch.empty_like, q) if out is None else out
+    lse = _new(side, q.new_empty, (B, Hq, 1), dtype=torch.float32) if lse is None else lse
     if _flat("out", out, torch.bfloat16, 4, dev) != qshape or _flat("lse", lse, torch.float32, 3, dev) != (B, Hq, 1):
         raise ValueError(f"out must be {tuple(qshape)} and lse {(B, Hq, 1)}")
     if workspace is None:
-        workspace = decode_prefix_workspace(B, Hq, Hkv, max_prefix_len, max_seq_len, q.device)
-        _used_on(stream, workspace)
+        workspace = _new(side, decode_prefix_workspace, B, Hq, Hkv, max_prefix_len, max_seq_len, q.device)
     ws_bytes, = _flat("workspace", workspace, torch.uint8, 1, dev)
     _call(load_library().attn_decode_prefix, dev, stream, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
           prefix_table.data_ptr(), prefix_len.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
