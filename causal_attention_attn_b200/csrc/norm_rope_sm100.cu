@@ -112,8 +112,8 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_kernel(const NormRopePa
             const uint32_t base = ring + static_cast<uint32_t>(s * G::kStageBytes);
             const int pos = p.positions ? __ldg(p.positions + tok) : static_cast<int>(a.i);
             a.has = p.table.has(pos);
-            // A row that does not exist, or whose position has no row of the tables, arrives as zeros (and
-            // gives zeros: consume takes r as 0 there).
+            // A row that does not exist, or whose position has no row of the tables, arrives as zeros; consume
+            // takes r as 0 there, which keeps it out of dw, and stores zeros (0 times a weight need not be 0).
             const bool on0 = a.live0 && a.has, on1 = a.live1 && a.has;
             if (kBackward) {
                 const __nv_bfloat16 *dz = sd.dz + a.offset(sd.zs);
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_kernel(const NormRopePa
                 if (turn)
                     rotate_pairs<false>(x[k], ang);
                 if (k ? a.live1 : a.live0)
-                    store_row(out + (k ? sd.os.h : 0), le, pack_pairs<kInterleaved>(x[k]));
+                    store_row(out + (k ? sd.os.h : 0), le, a.has ? pack_pairs<kInterleaved>(x[k]) : zero_row());
             }
         } else {
             // (One row after the other: both at once need more than 128 registers, and spilling took 1.7
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_kernel(const NormRopePa
                     }
                 }
                 if (live)
-                    store_row(out + (k ? sd.os.h : 0), le, pack_pairs<kInterleaved>(dy));
+                    store_row(out + (k ? sd.os.h : 0), le, a.has ? pack_pairs<kInterleaved>(dy) : zero_row());
             }
         }
     };
