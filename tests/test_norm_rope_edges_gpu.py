@@ -1,5 +1,5 @@
-"""attn_qk_norm_rope and its gradient where they can go wrong: weights that are not finite, against the plain
-64-bit forms with the error bounds of tests/rows_reference.py."""
+"""attn_qk_norm_rope and its gradient where they can go wrong: weights that are not finite, rows of eps's
+size, against the plain 64-bit forms with the error bounds of tests/rows_reference.py."""
 import pytest
 import torch
 
@@ -51,3 +51,56 @@ def test_rows_without_a_position_are_zeros_whatever_the_weights(D, interleaved):
     for i, (a, b) in enumerate(zip(x, dz)):  # the weights' gradient does not read the weights
         _, _, dw, bw = ref.backward(a, w[i], cos, sin, pos, interleaved, 1e-6, b)
         ref.within(back[2 + i], dw, bw)
+
+
+@pytest.mark.parametrize("scale,eps", [(1e-3, 1e-6), (1.0, 0.5), (3e-2, 1e-5), (1e-3, 1e-2)])
+@pytest.mark.parametrize("D,interleaved", [(32, False), (64, True), (128, False)])
+def test_rows_of_the_size_of_eps(D, interleaved, scale, eps):
+    """mean(x^2) next to eps or below it, and rows of zeros (0 / sqrt(eps) = 0; their gradient is w dy / sqrt(eps)).
+    That these sizes tell where eps goes: tests/test_rows_eps.py."""
+    B, Hq, Hkv, S = 2, 6, 3, 21
+    x, dz, w, cos, sin = make(B, Hq, Hkv, S, D, D, seed=D + int(1 / eps))
+    x = [(t.float() * scale).to(torch.bfloat16) for t in x]
+    for t in x:
+        t[0, 1, 3] = 0
+        t[1, :, 20] = 0
+    at = torch.arange(S).expand(B, S)
+    cu = lambda t: t.cuda()  # noqa: E731
+    kw = dict(q_weight=w[0].cuda(), k_weight=w[1].cuda(), interleaved=interleaved, eps=eps)
+    out = attn.attn_qk_norm_rope(*map(cu, x), cos.cuda(), sin.cuda(), **kw)
+    back = attn.attn_qk_norm_rope_bwd(*map(cu, x), cos.cuda(), sin.cuda(), *map(cu, dz), **kw)
+    for i in range(2):
+        ref.within(out[i], *ref.forward(x[i], w[i], cos, sin, at, interleaved, eps), f"forward {i}")
+        assert torch.all(out[i][0, 1, 3] == 0) and torch.all(out[i][1, :, 20] == 0)
+        dx, bx, dw, bw = ref.backward(x[i], w[i], cos, sin, at, interleaved, eps, dz[i])
+        ref.within(back[i], dx, bx, f"backward {i}")
+        ref.within(back[2 + i], dw, bw, f"weight {i}")
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("scale,eps", [(1e-3, 1e-6), (1.0, 0.5)])
+def test_append_of_rows_of_the_size_of_eps(scale, eps, fp8):
+    B, Hq, Hkv, S, D, page = 2, 4, 2, 16, 128, 16
+    x, _, w, cos, sin = make(B, Hq, Hkv, S, D, D, seed=77)
+    q, k = ((t.float() * scale).to(torch.bfloat16) for t in x)
+    k[0, 1, 3] = 0
+    table = torch.arange(B, dtype=torch.int32).view(B, 1).cuda()
+    lens = torch.full((B,), S, dtype=torch.int32).cuda()
+    pages = [torch.zeros((B, Hkv, page, D), dtype=torch.uint8 if fp8 else torch.bfloat16, device="cuda") for _ in range(2)]
+    coef = 2.0 ** -4
+    scales = [torch.full((Hkv, D), coef).cuda() for _ in range(2)] if fp8 else []
+    fn = attn.attn_append_paged_fp8 if fp8 else attn.attn_append_paged
+    q_out = fn(k.cuda(), k.cuda(), cos.cuda(), sin.cuda(), *pages, *scales, table, lens, q=q.cuda(), q_weight=w[0].cuda(),
+               k_weight=w[1].cuda(), eps=eps)
+    at = torch.arange(S).expand(B, S)
+    ref.within(q_out, *ref.forward(q, w[0], cos, sin, at, False, eps), "q")
+    kz, kb = ref.forward(k, w[1], cos, sin, at, False, eps)
+    if not fp8:
+        ref.within(pages[0], kz, kb, "k")
+        return
+    # Half a step of e4m3 (2^-4 of the binade's start, 2^-10 among its subnormals), the quotient's rounding (u) and
+    # the fp32 error of x (the bound without its bf16 part).
+    t = kz / coef
+    step = torch.exp2(torch.floor(torch.log2(t.abs().clamp(min=2.0 ** -6))) - 4)
+    ref.within(pages[0].view(torch.float8_e4m3fn).float(), t.clamp(-448, 448),
+               step + 2 * (kb - ref.BF16 * kz.abs()) / coef + ref.U * t.abs(), "k codes")
