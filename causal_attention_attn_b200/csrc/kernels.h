@@ -13,23 +13,21 @@ namespace attn_b200 {
 // Devices the library keeps state for (function attributes, occupancy, workspaces), by index.
 constexpr int kMaxDevices = 64;
 
-// Launches `kernel`; with `overlap`, programmatically behind the kernel before it on the stream: it may
-// start once that one's blocks all run (or have called griddepcontrol.launch_dependents), and what it
-// needs of it lies behind its own griddepcontrol.wait.
+// Launches `kernel` programmatically behind the kernel before it on the stream: it may start once that
+// one's blocks all run (or have called griddepcontrol.launch_dependents), and what it needs of it lies
+// behind its own griddepcontrol.wait.
 template <typename... Params, typename... Args>
-cudaError_t launch_behind(void (*kernel)(Params...), int grid, int threads, size_t smem, cudaStream_t stream, bool overlap,
-                          const Args &...args)
+cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t stream, const Args &...args)
 {
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(static_cast<unsigned>(threads));
-    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = &attr;
-    cfg.numAttrs = overlap ? 1 : 0;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 

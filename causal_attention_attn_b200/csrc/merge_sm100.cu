@@ -288,7 +288,7 @@ cudaError_t launch_prefix_merge(const PrefixMergeArgs &args, cudaStream_t stream
     const int rows = a.B * a.Hq;
     // Up to a block an SM's worth of rows or so, latency counts; beyond it, the work a row costs.
     const int split_blocks = rows, blocks = (rows + kMergeWarps - 1) / kMergeWarps;
-    auto launch = [&](auto kernel, int grid) { return launch_behind(kernel, grid, 32 * kMergeWarps, 0, stream, true, a); };
+    auto launch = [&](auto kernel, int grid) { return launch_behind(kernel, dim3(static_cast<unsigned>(grid)), 32 * kMergeWarps, stream, a); };
     if (rows <= kMergeSplitRows)
         return a.find ? launch(prefix_merge_kernel<kMergeWarps, true>, split_blocks)
                        : launch(prefix_merge_kernel<kMergeWarps, false>, split_blocks);

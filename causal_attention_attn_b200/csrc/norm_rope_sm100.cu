@@ -368,17 +368,9 @@ cudaError_t launch(const NormRopeArgs &a, cudaStream_t stream)
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !kBackward || !a.partials)
         return e;
-    // Programmatic launch: the second kernel's launch overlaps the first one's end.
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(D / 32, 2);
-    cfg.blockDim = dim3(1024);
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, weight_grad_kernel, static_cast<const float *>(a.partials), blocks, D, a.dwq, a.dwk);
+    // The second kernel's launch overlaps the first one's end.
+    return launch_behind(weight_grad_kernel, dim3(D / 32, 2), 1024, stream, static_cast<const float *>(a.partials), blocks, D,
+                         a.dwq, a.dwk);
 }
 
 template <int D>

@@ -13,6 +13,10 @@
 #include "kernels.h"
 
 namespace attn_b200 {
+
+// The workspace that callers size by the macro holds a partial of both weights' gradients for every block.
+static_assert(ATTN_QK_NORM_ROPE_BWD_WORKSPACE(128) == kNormRopeBwdBlocks * 2u * 128u * sizeof(float), "workspace of the gradient");
+
 namespace {
 
 bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
