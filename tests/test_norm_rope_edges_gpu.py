@@ -1,5 +1,5 @@
 """attn_qk_norm_rope and its gradient where they can go wrong: weights that are not finite, rows of eps's
-size, against the plain 64-bit forms with the error bounds of tests/rows_reference.py."""
+size, gradients written over the inputs, against the plain 64-bit forms with the error bounds of tests/rows_reference.py."""
 import pytest
 import torch
 
@@ -104,3 +104,20 @@ def test_append_of_rows_of_the_size_of_eps(scale, eps, fp8):
     step = torch.exp2(torch.floor(torch.log2(t.abs().clamp(min=2.0 ** -6))) - 4)
     ref.within(pages[0].view(torch.float8_e4m3fn).float(), t.clamp(-448, 448),
                step + 2 * (kb - ref.BF16 * kz.abs()) / coef + ref.U * t.abs(), "k codes")
+
+
+@pytest.mark.parametrize("norm", [True, False])
+@pytest.mark.parametrize("D,interleaved", [(32, False), (64, True), (128, False)])
+def test_gradients_written_over_the_inputs(D, interleaved, norm):
+    """dq may be q (and dk k) as well as dq_out: the same bits as in memory of their own."""
+    B, Hq, Hkv, S = 3, 7, 2, 210
+    x, dz, w, cos, sin = make(B, Hq, Hkv, S, D, D, seed=D + 1)
+    q, k, dqo, dko = (t.cuda() for t in (*x, *dz))
+    kw = dict(q_weight=w[0].cuda() if norm else None, k_weight=w[1].cuda() if norm else None, interleaved=interleaved)
+    want = attn.attn_qk_norm_rope_bwd(q, k, cos.cuda(), sin.cuda(), dqo, dko, **kw)
+    fused = torch.cat((q, k), dim=1).transpose(1, 2).contiguous()  # token-major, as a projection leaves it
+    qv, kv = fused[:, :, :Hq].transpose(1, 2), fused[:, :, Hq:].transpose(1, 2)
+    over = attn.attn_qk_norm_rope_bwd(qv, kv, cos.cuda(), sin.cuda(), dqo, dko, dq=qv, dk=kv, **kw)
+    assert over[0] is qv and over[1] is kv
+    for a, b in zip(over, want):
+        assert a is None and b is None or torch.equal(a, b)
