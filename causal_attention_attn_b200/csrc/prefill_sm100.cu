@@ -183,8 +183,8 @@ __device__ __forceinline__ float4 ld_shared4(uint32_t addr)
 }
 
 // Reference max of a row that has seen no key yet (paged variant): finite, so that the weights of
-// masked scores are 2^(-inf) = 0 rather than NaN, and far below any real score.
-constexpr float kNoKeyMax = -1e30f;
+// masked scores are 2^(-inf) = 0 rather than NaN, and at the end of fp32, below any finite score.
+constexpr float kNoKeyMax = -3.4e38f;
 
 __device__ __forceinline__ float ex2(float x)
 {

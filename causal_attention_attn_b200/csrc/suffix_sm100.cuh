@@ -54,8 +54,9 @@ constexpr int kOffLen = kOffUnits + 4 * (kPagedMaxBatch + 1);    // clamped leng
 constexpr int kSmem = kOffLen + 4 * kPagedMaxBatch + 1024;  // + alignment of the base
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
 constexpr float kRescaleThreshold = 8.0f;
-// Floor of the reference max: finite, so that a row of scores -inf has weights 0, not NaN.
-constexpr float kNoKeyMax = -1e30f;
+// Floor of the reference max: finite, so that a row of scores -inf has weights 0, not NaN, and at the end of
+// fp32, below any finite score.
+constexpr float kNoKeyMax = -3.4e38f;
 
 struct SuffixParams {
     const __nv_bfloat16 *q;
