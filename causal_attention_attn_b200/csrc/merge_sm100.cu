@@ -286,7 +286,11 @@ cudaError_t launch_prefix_merge(const PrefixMergeArgs &args, cudaStream_t stream
     a.by_pair = FastDiv(a.suffix.heads_per_pair);
     static_assert(32 * kMergeWarps == 128, "one thread a channel");
     const int rows = a.B * a.Hq;
-    // Up to a block an SM's worth of rows or so, latency counts; beyond it, the work a row costs.
+    // Four warps a row shorten the chain of a row's parts, one costs fewer blocks. Measured with either
+    // behind 4,096 + 256 keys (about 18 parts a row), 32 query and 8 kv heads: 128 rows 12.2 us a call with four
+    // and 14.5 with one, 768 rows 14.8 and 15.7, 1,024 rows 17.0 and 17.4, 1,280 rows 20.0 and 18.8, 4,096 rows
+    // 47 and 37. (Rows of few parts, behind 512 keys, were faster with one at any count: 128 rows 9.6 and
+    // 8.9, 1,024 rows 12.1 and 10.6.)
     const int split_blocks = rows, blocks = (rows + kMergeWarps - 1) / kMergeWarps;
     auto launch = [&](auto kernel, int grid) { return launch_behind(kernel, dim3(static_cast<unsigned>(grid)), 32 * kMergeWarps, stream, a); };
     if (rows <= kMergeSplitRows)

@@ -7,9 +7,11 @@ products (<= 10 u, halved by the root), mean and eps 2 u, rsqrtf 4 u, two produc
 the rotation adds two products, one addition: 3 u of |y_a c| + |y_b s|. Together 17 u of that sum;
 FORWARD_U = 20. Backward: dy 3 u, g 1 u, the sum of g x 10 u + 2, r three times 14 u in r^3 (f has r^2,
 the factor outside r), four more roundings: below 64 u of the sum of magnitudes; BACKWARD_U = 64.
-dw: a term is off by at most 3 + 14 + 2 u; the sums run through chains of at most 4 rows of a lane
-for the sizes tested (or rows / (592 * 8) beyond), 32 lanes and warps, 19 partials and 32 warps: below
-128 u; WEIGHT_U = 160 of the sum of the terms' magnitudes.
+dw: a term is off by at most 3 + 14 + 2 u. The sum runs through chains of: the rows of one lane (n),
+the 32 / (D / 16) lane groups of a warp (at most 4 additions), 8 warps, the blocks' partials 128 apart (at most
+5 of 592), 2 shuffles and 32 warps: n + 51 u. A lane takes two rows of each unit of its warp, and there are
+min(2 per SM, 592) blocks of 8 warps: 6 rows for 1,500 tokens of 32 heads of 128, and at most 88 up to
+830,000 rows of a side. So below 19 + 51 + 90 u; WEIGHT_U = 160 of the sum of the terms' magnitudes.
 """
 import torch
 

@@ -125,3 +125,17 @@ def test_results_that_the_current_stream_reads_are_not_handed_to_the_next_call(n
     again = second(side)             # not ordered behind the reads
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(kept, want)) and len(again) == len(want)
+
+
+def test_host_buffers_through_another_stream():
+    """attn_fwd_host's staging memory, when it is not given, belongs to the call's stream as well."""
+    g = torch.Generator().manual_seed(7)
+    q, k, v = (torch.randn((1, h, 96, D), generator=g).to(torch.bfloat16).pin_memory() for h in (HQ, HKV, HKV))
+    want = attn.attn_fwd_host(q, k, v)
+    side = torch.cuda.Stream()
+    torch.cuda._sleep(DELAY)
+    for stream in (side, torch.cuda.ExternalStream(side.cuda_stream)):
+        got = attn.attn_fwd_host(q, k, v, stream=stream)
+        mine = [torch.full((1, h, 96, D), 7.0, dtype=torch.bfloat16, device="cuda") for h in (HQ, HKV, HKV, HQ)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)) and all(torch.all(t == 7) for t in mine)
