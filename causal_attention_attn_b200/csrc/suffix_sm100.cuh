@@ -8,8 +8,9 @@
  * heads), its keys are units of 16, all pairs' units are laid end to end, two more before each pair for
  * what its start and end cost a warp, and cut evenly over the warps of the grid (EvenRange). Each warp
  * streams its units through a ring of its own by TMA and no warp waits for another, so the start and the
- * end of a pair are hidden behind the other eleven warps of the SM. (The CTA-wide paged decode kernel, whose 128-key chunks pass through one softmax, took 53 us where
- * this takes 31, for 125 sequences of up to 768 keys and 6 kv heads: it drains at every pair.)
+ * end of a pair are hidden behind the other eleven warps of the SM. (The CTA-wide paged decode kernel, whose
+ * 128-key chunks pass through one softmax, took 53 us where this takes 31, for 125 sequences of up to 768
+ * keys and 6 kv heads: it drains at every pair.)
  *
  * Per unit, K and V [16 keys][128] in shared memory (128-byte swizzle), heads in groups of eight:
  *   S^T = K Q^T       mma m16n8k16: A = K (ldmatrix), B = Q^T from registers; thread t holds keys t / 4

@@ -493,6 +493,9 @@ int attn_append_paged_fp8(const void *q, const void *k, const void *v, const voi
  *                    aligned, owned by the caller and used only until the call's work is done; its
  *                    contents need not be kept or cleared. Calls that overlap need one each; a captured
  *                    call keeps using the one it was given.
+ * As in the other calls over a bf16 cache, scores, sums and the joining of the parts are fp32 and the
+ * softmax weights are rounded to bf16 for the product with V (O is divided by the sum of the rounded
+ * weights, lse comes from the fp32 ones).
  * A sequence with neither prefix nor suffix keys gets o = 0 and lse = -inf. Table entries outside
  * [0, num_pages) read as zeros. bf16 cache, head dim 128, 1 <= B <= 1024, B * Hq <= 2^22, Hq % Hkv == 0.
  * Lengths and tables are read on the device, never on the host. Never allocates or synchronises; the
