@@ -133,18 +133,25 @@ def _side(stream, dev: int):
     return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle, device=dev)
 
 
-def _new(side, make, *args, **kw):
-    """Memory that this module allocates for a call: make(...). The caching allocator orders a block's
-    next use behind the stream that it was allocated on, so with a `side` stream it is that stream's block:
-    what had it before is behind the call, and what gets it when it is dropped, behind the call too. The
-    current stream, where a result is usually read next, is recorded beside it."""
+def _made(side, *slots):
+    """The tensors of a call, each slot (the caller's or None; what makes one; of what). The caching
+    allocator orders a block's next use behind the stream that it was allocated on, so with a `side` stream
+    what is made is that stream's: what had the block before is behind the call, and what gets it when the
+    result is dropped, behind the call too. The current stream, where a result is usually read next, is
+    recorded beside it."""
     if side is None:
-        return make(*args, **kw)
+        return [make(of) if given is None else given for given, make, of in slots]
     current = torch.cuda.current_stream(side.device)
     with torch.cuda.stream(side):
-        t = make(*args, **kw)
-    t.record_stream(current)
-    return t
+        made = [make(of) if given is None else given for given, make, of in slots]
+    for t, slot in zip(made, slots):
+        if slot[0] is None:
+            t.record_stream(current)
+    return made
+
+
+def _lse_of(q):
+    return torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
 
 
 def _check_tensor(name, t, dtype, ndim):
@@ -213,19 +220,15 @@ def attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: float | N
         raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}")
     if scale is None:
         scale = D ** -0.5
-    side = _side(stream, q.get_device())
-    if out is None:
-        out = _new(side, torch.empty, q.shape, dtype=torch.bfloat16, device=q.device)
-    else:
+    if out is not None:
         _check_rows("out", out, torch.bfloat16)
         if out.shape != q.shape:
             raise ValueError("out must have the shape of q")
-    if lse is None:
-        lse = _new(side, torch.empty, (B, Hq, Sq), dtype=torch.float32, device=q.device)
-    else:
+    if lse is not None:
         _check_tensor("lse", lse, torch.float32, 3)
         if tuple(lse.shape) != (B, Hq, Sq):
             raise ValueError("lse must be [B, Hq, Sq]")
+    out, lse = _made(_side(stream, q.get_device()), (out, _new_rows, q), (lse, _lse_of, q))
     strided = not all(t.is_contiguous() for t in (q, k, v, out))
     with torch.cuda.device(q.device):
         if strided:
@@ -265,10 +268,9 @@ def attn_fwd_host(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: floa
     stream = stream or torch.cuda.current_stream(device)
     if dev_bufs is None:
         dev = torch.device(device).index
-        side = _side(stream, torch.cuda.current_device() if dev is None else dev)
-        dev_bufs = [_new(side, torch.empty, shape, dtype=torch.bfloat16, device=device)
-                    for shape in (q.shape, k.shape, v.shape, q.shape)]
-        dev_bufs.append(_new(side, torch.empty, (B, Hq, Sq), dtype=torch.float32, device=device))
+        slots = [(None, functools.partial(torch.empty, dtype=torch.bfloat16, device=device), t.shape) for t in (q, k, v, q)]
+        slots.append((None, functools.partial(torch.empty, dtype=torch.float32, device=device), q.shape[:3]))
+        dev_bufs = _made(_side(stream, torch.cuda.current_device() if dev is None else dev), *slots)
     qd, kd, vd, od, ld = dev_bufs
     if out_host is None:
         out_host = torch.empty(q.shape, dtype=torch.bfloat16, pin_memory=True)
@@ -301,9 +303,7 @@ def attn_decode_noalloc(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale
         raise ValueError(f"expected q [B,Hq,1,D] and k, v [B,Hkv,Skv,D]; got {tuple(q.shape)}, {tuple(k.shape)}")
     if scale is None:
         scale = D ** -0.5
-    side = _side(stream, q.get_device())
-    out = _new(side, torch.empty_like, q) if out is None else out
-    lse = _new(side, torch.empty, (B, Hq, 1), dtype=torch.float32, device=q.device) if lse is None else lse
+    out, lse = _made(_side(stream, q.get_device()), (out, torch.empty_like, q), (lse, _lse_of, q))
     _check_tensor("out", out, torch.bfloat16, 4)
     _check_tensor("lse", lse, torch.float32, 3)
     with torch.cuda.device(q.device):
@@ -336,9 +336,7 @@ def attn_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Ten
         raise ValueError("block_table and seq_lens need one row / entry per batch element")
     if scale is None:
         scale = D ** -0.5
-    side = _side(stream, q.get_device())
-    out = _new(side, torch.empty_like, q) if out is None else out
-    lse = _new(side, torch.empty, (B, Hq, 1), dtype=torch.float32, device=q.device) if lse is None else lse
+    out, lse = _made(_side(stream, q.get_device()), (out, torch.empty_like, q), (lse, _lse_of, q))
     _check_tensor("out", out, torch.bfloat16, 4)
     _check_tensor("lse", lse, torch.float32, 3)
     with torch.cuda.device(q.device):
@@ -373,9 +371,7 @@ def attn_prefill_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Te
         raise ValueError("block_table and seq_lens need one row / entry per batch element")
     if scale is None:
         scale = D ** -0.5
-    side = _side(stream, q.get_device())
-    out = _new(side, torch.empty_like, q) if out is None else out
-    lse = _new(side, torch.empty, (B, Hq, Sq), dtype=torch.float32, device=q.device) if lse is None else lse
+    out, lse = _made(_side(stream, q.get_device()), (out, torch.empty_like, q), (lse, _lse_of, q))
     _check_tensor("out", out, torch.bfloat16, 4)
     _check_tensor("lse", lse, torch.float32, 3)
     with torch.cuda.device(q.device):
@@ -413,9 +409,7 @@ def attn_decode_fp8(q: torch.Tensor, k8: torch.Tensor, v8: torch.Tensor, k_scale
         raise ValueError("expected q [B,Hq,1,D], k8, v8 [B,Hkv,Skv,D] and scales [Hkv,D]")
     if scale is None:
         scale = D ** -0.5
-    side = _side(stream, q.get_device())
-    out = _new(side, torch.empty_like, q) if out is None else out
-    lse = _new(side, torch.empty, (B, Hq, 1), dtype=torch.float32, device=q.device) if lse is None else lse
+    out, lse = _made(_side(stream, q.get_device()), (out, torch.empty_like, q), (lse, _lse_of, q))
     _check_tensor("out", out, torch.bfloat16, 4)
     _check_tensor("lse", lse, torch.float32, 3)
     with torch.cuda.device(q.device):
@@ -443,9 +437,7 @@ def attn_prefill_fp8(q: torch.Tensor, k8: torch.Tensor, v8: torch.Tensor, k_scal
         raise ValueError("expected q [B,Hq,Sq,D], k8, v8 [B,Hkv,Skv,D] and scales [Hkv,D]")
     if scale is None:
         scale = D ** -0.5
-    side = _side(stream, q.get_device())
-    out = _new(side, torch.empty_like, q) if out is None else out
-    lse = _new(side, torch.empty, (B, Hq, Sq), dtype=torch.float32, device=q.device) if lse is None else lse
+    out, lse = _made(_side(stream, q.get_device()), (out, torch.empty_like, q), (lse, _lse_of, q))
     _check_tensor("out", out, torch.bfloat16, 4)
     _check_tensor("lse", lse, torch.float32, 3)
     with torch.cuda.device(q.device):
@@ -477,9 +469,7 @@ def attn_decode_paged_fp8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch
         raise ValueError("block_table and seq_lens need one row / entry per batch element")
     if scale is None:
         scale = D ** -0.5
-    side = _side(stream, q.get_device())
-    out = _new(side, torch.empty_like, q) if out is None else out
-    lse = _new(side, torch.empty, (B, Hq, 1), dtype=torch.float32, device=q.device) if lse is None else lse
+    out, lse = _made(_side(stream, q.get_device()), (out, torch.empty_like, q), (lse, _lse_of, q))
     _check_tensor("out", out, torch.bfloat16, 4)
     _check_tensor("lse", lse, torch.float32, 3)
     with torch.cuda.device(q.device):
@@ -532,10 +522,8 @@ def attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
         raise ValueError("shapes of q, k, v, o, lse, dout disagree")
     if scale is None:
         scale = D ** -0.5
-    side = _side(stream, q.get_device())
-    dq = _new(side, torch.empty_like, q) if dq is None else dq
-    dk = _new(side, torch.empty_like, k) if dk is None else dk
-    dv = _new(side, torch.empty_like, v) if dv is None else dv
+    dq, dk, dv = _made(_side(stream, q.get_device()), (dq, torch.empty_like, q), (dk, torch.empty_like, k),
+                       (dv, torch.empty_like, v))
     with torch.cuda.device(q.device):
         rc = load_library().attn_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dout.data_ptr(),
                                      lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Hq, Hkv, Sq, Skv, D,
@@ -634,8 +622,20 @@ def _positions(positions, B, S, dev):
     return positions.data_ptr()
 
 
-def _new_rows(like, side):
-    return _new(side, torch.empty_like, like, memory_format=torch.contiguous_format)
+def _new_rows(like):
+    return torch.empty_like(like, memory_format=torch.contiguous_format)
+
+
+def _weight_grad_of(weight):
+    return torch.empty_like(weight, dtype=torch.float32)
+
+
+def _bwd_workspace_of(weight):
+    return torch.empty(_NORM_ROPE_BWD_BLOCKS * 2 * weight.shape[0], dtype=torch.float32, device=weight.device)
+
+
+def _prefix_workspace_of(sizes):
+    return decode_prefix_workspace(*sizes)
 
 
 def attn_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor | None, sin: torch.Tensor | None,
@@ -659,9 +659,8 @@ def attn_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor | None
         raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}")
     rot_dim, max_pos = _rotation(cos, sin, D, dev)
     qw, kw, pos = _weight("q_weight", q_weight, D, dev), _weight("k_weight", k_weight, D, dev), _positions(positions, B, S, dev)
-    side = _side(stream, dev)
-    q_out = _new_rows(q, side) if q_out is None else q_out
-    k_out = _new_rows(k, side) if k_out is None else k_out
+    if q_out is None or k_out is None:
+        q_out, k_out = _made(_side(stream, dev), (q_out, _new_rows, q), (k_out, _new_rows, k))
     _, qos = _rows("q_out", q_out, dev, qshape)
     _, kos = _rows("k_out", k_out, dev, kshape)
     _call(load_library().attn_qk_norm_rope, dev, stream, q.data_ptr(), k.data_ptr(), qw, kw, _ptr(cos), _ptr(sin), pos,
@@ -690,14 +689,14 @@ def attn_qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor | 
     rot_dim, max_pos = _rotation(cos, sin, D, dev)
     qw, kw, pos = _weight("q_weight", q_weight, D, dev), _weight("k_weight", k_weight, D, dev), _positions(positions, B, S, dev)
     side = _side(stream, dev)
-    dq = _new_rows(q, side) if dq is None else dq
-    dk = _new_rows(k, side) if dk is None else dk
+    if dq is None or dk is None:
+        dq, dk = _made(side, (dq, _new_rows, q), (dk, _new_rows, k))
     _, dqs = _rows("dq", dq, dev, qshape)
     _, dks = _rows("dk", dk, dev, kshape)
     dwq = dwk = ws = None
     if qw is not None and kw is not None:  # (one alone: the library refuses it)
-        dwq, dwk = (_new(side, torch.empty_like, w, dtype=torch.float32) for w in (q_weight, k_weight))
-        ws = _new(side, torch.empty, _NORM_ROPE_BWD_BLOCKS * 2 * D, dtype=torch.float32, device=q.device)
+        dwq, dwk, ws = _made(side, (None, _weight_grad_of, q_weight), (None, _weight_grad_of, k_weight),
+                             (None, _bwd_workspace_of, q_weight))
     _call(load_library().attn_qk_norm_rope_bwd, dev, stream, q.data_ptr(), k.data_ptr(), qw, kw, _ptr(cos), _ptr(sin), pos,
           dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), _ptr(dwq), _ptr(dwk), _ptr(ws), B, Hq, Hkv, S,
           D, qs, ks, dqos, dkos, dqs, dks, rot_dim, max_pos, 1 if interleaved else 0, eps)
@@ -735,7 +734,8 @@ def _append(k, v, cos, sin, k_pages, v_pages, k_scale, v_scale, block_table, seq
         Bq, Hq, S, Dq = qshape
         if Bq != B or S != Sq or Dq != D:
             raise ValueError(f"q must be [{B}, Hq, {Sq}, {D}], got {tuple(q.shape)}")
-        q_out = _new_rows(q, _side(stream, dev)) if q_out is None else q_out
+        if q_out is None:
+            q_out, = _made(_side(stream, dev), (None, _new_rows, q))
         _, qos = _rows("q_out", q_out, dev, qshape)
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -820,13 +820,11 @@ def attn_decode_prefix(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Te
         raise ValueError("block_table and seq_lens need one row / entry per batch element, prefix_len one entry")
     if scale is None:
         scale = D ** -0.5
-    side = _side(stream, dev)
-    out = _new(side, torch.empty_like, q) if out is None else out
-    lse = _new(side, q.new_empty, (B, Hq, 1), dtype=torch.float32) if lse is None else lse
+    if out is None or lse is None or workspace is None:
+        out, lse, workspace = _made(_side(stream, dev), (out, torch.empty_like, q), (lse, _lse_of, q),
+                                    (workspace, _prefix_workspace_of, (B, Hq, Hkv, max_prefix_len, max_seq_len, q.device)))
     if _flat("out", out, torch.bfloat16, 4, dev) != qshape or _flat("lse", lse, torch.float32, 3, dev) != (B, Hq, 1):
         raise ValueError(f"out must be {tuple(qshape)} and lse {(B, Hq, 1)}")
-    if workspace is None:
-        workspace = _new(side, decode_prefix_workspace, B, Hq, Hkv, max_prefix_len, max_seq_len, q.device)
     ws_bytes, = _flat("workspace", workspace, torch.uint8, 1, dev)
     _call(load_library().attn_decode_prefix, dev, stream, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
           prefix_table.data_ptr(), prefix_len.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),

@@ -139,3 +139,30 @@ def test_host_buffers_through_another_stream():
         mine = [torch.full((1, h, 96, D), 7.0, dtype=torch.bfloat16, device="cuda") for h in (HQ, HKV, HKV, HQ)]
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want)) and all(torch.all(t == 7) for t in mine)
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_a_captured_fork(name):
+    """A capture that forks to another stream, where the call runs and its first results are dropped: the graph's
+    replays give the call's results, and what the capture's own stream makes meanwhile is not written over."""
+    fn = calls()[name]
+    want = [t.clone() for t in fn(None)]
+    side = torch.cuda.Stream()
+    fn(side)  # workspaces are in place before the capture
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000)
+        fn(side)
+        mine = [torch.full_like(t, 7) for t in want for _ in range(3)]
+        got = fn(side)
+        main.wait_stream(side)
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)) and all(torch.all(t == 7) for t in mine)
